@@ -63,6 +63,7 @@ typedef enum { BFMOE_F32 = 0, BFMOE_BF16 = 1 } bfmoe_dtype;
 #define BFMOE_MAX_D 4096        /* d: power of two, 4 <= d <= 4096         */
 #define BFMOE_MAX_EXPERTS 4096  /* N: 1 <= N <= 4096                       */
 #define BFMOE_MAX_K 8           /* k: 1 <= k <= min(8, N)                  */
+#define BFMOE_MAX_GROUPS 64     /* expert groups of bfmoe_route            */
 
 /* One ButterflyMoE layer (all pointers device, caller-owned, read-only). */
 typedef struct {
@@ -341,6 +342,154 @@ size_t bfmoe_backward_workspace_size(int d, int n_experts, int T, int k);
  */
 int bfmoe_decode_forward(const bfmoe_layer* layer, const void* x, int x_dtype, int T, int k,
                          const int32_t* idx, const float* gates, void* y, bfmoe_stream_t stream);
+
+/* ---- routing from logits, its gradient and its losses --------------------- */
+
+/*
+ * Router logits l = x W_g^T (+ b) alone, float32 [T][N]: those of
+ * bfmoe_router_topk (the tensor-core router for bfloat16 tokens with d a
+ * multiple of 64, the CUDA cores otherwise), for bfmoe_route and its losses.
+ * A NaN logit may come out as -inf (both mean a masked expert).
+ *   logits    device float [T][N] (written), 32-byte aligned
+ *   ws        device scratch, bfmoe_workspace_size(d, N, T, 1, x_dtype) bytes
+ * Other arguments as for bfmoe_router_topk.
+ */
+int bfmoe_router_logits(const void* x, int x_dtype, int T, int d, const float* w_gate, const float* bias,
+                        int n_experts, float* logits, void* ws, size_t ws_bytes, bfmoe_stream_t stream);
+
+typedef enum { BFMOE_SCORE_SOFTMAX = 0, BFMOE_SCORE_SIGMOID = 1 } bfmoe_score;
+typedef enum { BFMOE_GROUP_MAX = 0, BFMOE_GROUP_TOP2 = 1 } bfmoe_group_score;
+
+/* How logits become experts and gates (bfmoe_route). */
+typedef struct {
+  int score;        /* bfmoe_score: softmax over the N logits, or sigmoid of each */
+  int n_groups;     /* groups of N / n_groups consecutive experts (divides N)     */
+  int top_groups;   /* groups kept per token, 1 <= top_groups <= n_groups         */
+  int group_score;  /* bfmoe_group_score: a group's largest value, or the sum of
+                       its two best scores (+ balance bias)                       */
+  int renormalize;  /* gates over their sum (not 0) or as the scores are (0)      */
+  float scale;      /* multiplies the gates                                       */
+} bfmoe_scoring;
+
+/*
+ * Experts and gates from logits.  The pages define expert selection in general
+ * only (signalfieldnotes ButterflyMoE article, glossary "Mixtures of
+ * Experts"); bfmoe_router_topk is the plain softmax form, this call the others.
+ *   - An expert is masked where its logit is NaN or -inf.  softmax:
+ *     p_e = exp(l_e) / sum over the unmasked (logits of +inf share the mass);
+ *     sigmoid: s_e = 1 / (1 + exp(-l_e)).
+ *   - The value that ranks an expert is its logit, or score + balance_bias[e]
+ *     when a bias is given (a NaN or -inf value masks the expert too, without
+ *     taking it out of the softmax).
+ *   - With n_groups > top_groups the best groups are kept: by their largest
+ *     value, or by the sum of their two best scores (+ bias) (one, if one
+ *     expert is left; a group with none ranks last), the lower group first on
+ *     equal sums.
+ *   - The k largest values of the kept groups are chosen, in descending
+ *     order, the lower index first on equal values; masked experts fill up
+ *     last, by index.  The decisions are those of the values computed in 64
+ *     bits from the given logits and bias.
+ *   - gates: the scores of the chosen (no bias; 0 for a masked expert), over
+ *     their sum when renormalize (all 0 where nothing is left), times scale.
+ *   logits    device [T] rows of N, ld elements apart (ld >= N), dtype
+ *   balance_bias  device float [N] or NULL
+ *   idx, gates, counts, offsets, rows: as bfmoe_router_topk writes them; the
+ *             last three may all be NULL (then no workspace is needed)
+ *   ws        device scratch, bfmoe_route_workspace_size(N, T, k) bytes,
+ *             256-byte aligned
+ * idx and the buckets go to bfmoe_forward, bfmoe_decode_forward (idx) and
+ * bfmoe_expert_backward.
+ */
+int bfmoe_route(const void* logits, int dtype, int T, long long ld, int n_experts, int k,
+                const bfmoe_scoring* scoring, const float* balance_bias, int32_t* idx, float* gates,
+                int32_t* counts, int32_t* offsets, int32_t* rows, void* ws, size_t ws_bytes,
+                bfmoe_stream_t stream);
+
+/*
+ * The losses that keep a trained router's experts in use, over the R rows
+ * with at least one unmasked logit:
+ *   loss[0]  balance: N sum_e f_e P_e, f_e = load_e / (k R) the share of the
+ *            chosen slots that went to expert e, P_e the mean over the rows of
+ *            the scores over their sum
+ *   loss[1]  z: the mean of logsumexp(l)^2
+ *   logits, ld, dtype, T, N, k, idx as for bfmoe_route; score: bfmoe_score
+ *   loss      device float [2] (written)
+ *   load      device int32 [N + 1] (written): load_e, then R.  Loads of
+ *             several ranks may be added up before bfmoe_route_backward.
+ *   ws        as for bfmoe_route
+ * Sums are float64 across rows of blocks, in a fixed order.
+ */
+int bfmoe_balance_loss(const void* logits, int dtype, int T, long long ld, int n_experts, int k, int score,
+                       const int32_t* idx, float* loss, int32_t* load, void* ws, size_t ws_bytes,
+                       bfmoe_stream_t stream);
+
+/*
+ * Gradient of the logits: through the gates of bfmoe_route (the choice is
+ * held, as in bfmoe_backward) and through the two losses, in one pass.
+ *   idx       device int32 [T][k]: the routing (may be NULL without dgates)
+ *   dgates    device float [T][k]: the gradient of the gates, or NULL
+ *   load      device int32 [N + 1] of bfmoe_balance_loss, or NULL (no losses)
+ *   dloss     device float [2]: the gradients of loss[0] and loss[1]; given
+ *             with load
+ *   dlogits   device [T] rows of N, ld_dlogits apart, dtype of the logits
+ *             (written, 0 for masked experts); may be the logits themselves
+ * An index out of range is skipped and recorded as BFMOE_EDEVICE_BOUNDS.
+ * What is left of the router's gradient are plain matrix products:
+ * dW_g = dlogits^T x, db = column sums, dx += dlogits W_g.
+ */
+int bfmoe_route_backward(const void* logits, int dtype, int T, long long ld, int n_experts, int k,
+                         const bfmoe_scoring* scoring, const int32_t* idx, const float* dgates,
+                         const int32_t* load, const float* dloss, void* dlogits, long long ld_dlogits,
+                         bfmoe_stream_t stream);
+
+/* Scratch bytes of bfmoe_route and bfmoe_balance_loss (0 for invalid sizes). */
+size_t bfmoe_route_workspace_size(int n_experts, int T, int k);
+
+/*
+ * bfmoe_backward without the router: the gradients of the experts, and
+ *   dgates    device float [T][k] (written): <v_r, gy_t>, the gradient of each
+ *             gate, for bfmoe_route_backward
+ *   dx        device float [T][d] (written): the experts' part alone
+ * Other arguments and the workspace as for bfmoe_backward.
+ */
+int bfmoe_expert_backward(const bfmoe_layer* layer, const void* x, int x_dtype, int T, int k, const int32_t* idx,
+                          const float* gates, const int32_t* offsets, const int32_t* rows, const float* gy, float* dx,
+                          float* dtheta, float* dphi, float* dw_base, float* dalpha, float* dgates, void* ws,
+                          size_t ws_bytes, bfmoe_stream_t stream);
+
+/* ---- global gradient norm -------------------------------------------------- */
+
+/* One tensor of a list: len contiguous elements. */
+typedef struct {
+  void* grad;      /* device; read, and scaled in place when out is NULL     */
+  void* out;       /* device or NULL: where bfmoe_grad_clip writes instead   */
+  long long len;   /* elements (0 allowed)                                   */
+  int dtype;       /* bfmoe_dtype of grad                                    */
+  int out_dtype;   /* bfmoe_dtype of out                                     */
+} bfmoe_grad;
+
+/*
+ * norm = sqrt of the sum of the squares of every element of the list, summed
+ * in float64 in a fixed order and rounded once.
+ *   grads     host array of n (up to 32768) tensors, read during the call only
+ *   norm      device float [1] (written)
+ *   ws        device scratch, bfmoe_grad_workspace_size() bytes, 256-byte
+ *             aligned
+ */
+int bfmoe_grad_norm(const bfmoe_grad* grads, int n, float* norm, void* ws, size_t ws_bytes, bfmoe_stream_t stream);
+
+/*
+ * The norm, and every gradient times min(1, max_norm / norm): in place, or
+ * written to out (then out holds the gradients also where nothing is scaled).
+ * A norm that is not finite scales nothing; it is there to be read in norm.
+ * Tensors that the call writes may overlap no other tensor of the list
+ * (BFMOE_EINVAL).  max_norm >= 0.  Other arguments as for bfmoe_grad_norm.
+ */
+int bfmoe_grad_clip(const bfmoe_grad* grads, int n, float max_norm, float* norm, void* ws, size_t ws_bytes,
+                    bfmoe_stream_t stream);
+
+/* Scratch bytes of bfmoe_grad_norm and bfmoe_grad_clip. */
+size_t bfmoe_grad_workspace_size(void);
 
 /*
  * Form expert e densely, alpha * B(phi_e) . W_base . B(theta_e)^T, in float32

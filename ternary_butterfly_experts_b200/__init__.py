@@ -24,6 +24,9 @@ __all__ = [
     "bfmoe_router_topk_noalloc", "bfmoe_moe_forward", "bfmoe_moe_workspace_size", "bfmoe_prepare_layer",
     "bfmoe_layer_tables_size", "bfmoe_prepare_gate", "bfmoe_gate_parts_size", "bfmoe_backward", "bfmoe_backward_workspace_size",
     "bfmoe_forward", "bfmoe_decode_forward", "bfmoe_materialize_expert", "bfmoe_workspace_size", "bfmoe_router_scratch_size", "bfmoe_check_device_error",
+    "Scoring", "GradList", "bfmoe_router_logits", "bfmoe_route", "bfmoe_route_backward", "bfmoe_balance_loss",
+    "bfmoe_route_workspace_size", "bfmoe_expert_backward", "bfmoe_grad_norm", "bfmoe_grad_clip",
+    "bfmoe_grad_workspace_size",
     "bfmoe_launch_count", "bfmoe_profile_enable", "bfmoe_profile_collect", "bfmoe_last_error", "workspace",
 ]
 
@@ -383,6 +386,292 @@ def bfmoe_moe_forward_host(layer: Layer, x_host, w_gate, bias, k: int, y_host, w
     return y_host
 
 
+class Scoring:
+    """How logits become experts and gates (bfmoe_scoring in include/bfmoe.h):
+    ``score`` "softmax" or "sigmoid"; ``n_groups`` groups of consecutive
+    experts of which ``top_groups`` are kept by their largest value
+    (``group_score`` "max") or their two best scores ("top2"); gates over
+    their sum (``renormalize``) or as the scores are; times ``scale``."""
+
+    SCORES = {"softmax": capi.BFMOE_SCORE_SOFTMAX, "sigmoid": capi.BFMOE_SCORE_SIGMOID}
+    GROUP_SCORES = {"max": capi.BFMOE_GROUP_MAX, "top2": capi.BFMOE_GROUP_TOP2}
+
+    def __init__(self, score: str = "softmax", n_groups: int = 1, top_groups: int = 1, group_score: str = "max",
+                 renormalize: bool = True, scale: float = 1.0):
+        if score not in self.SCORES:
+            raise ValueError(f"score must be one of {sorted(self.SCORES)}, got {score!r}")
+        if group_score not in self.GROUP_SCORES:
+            raise ValueError(f"group_score must be one of {sorted(self.GROUP_SCORES)}, got {group_score!r}")
+        self.score, self.n_groups, self.top_groups, self.group_score = score, n_groups, top_groups, group_score
+        self.renormalize, self.scale = bool(renormalize), float(scale)
+        self.c = capi.BfmoeScoring(self.SCORES[score], n_groups, top_groups, self.GROUP_SCORES[group_score],
+                                   int(self.renormalize), self.scale)
+
+    def __repr__(self):
+        return (f"Scoring(score={self.score!r}, n_groups={self.n_groups}, top_groups={self.top_groups}, "
+                f"group_score={self.group_score!r}, renormalize={self.renormalize}, scale={self.scale})")
+
+
+def _here(stream, *named):
+    """The stream handle of a call whose tensors (name, tensor or None) must
+    all live on the current CUDA device."""
+    torch = _torch()
+    for name, t in named:
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+    dev = torch.cuda.current_device()
+    for name, t in named:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    return _stream(stream)
+
+
+def _need_shape(t, name, dtype, shape):
+    if t is None:
+        return
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+
+
+def _logits(t, name="logits"):
+    """(dtype code, T, N, row stride) of logits: rows of consecutive elements."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [T][N]")
+    T, N = t.shape
+    if N > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have consecutive elements in a row")
+    ld = t.stride(0) if T > 1 else N
+    if ld < N:
+        raise ValueError(f"the rows of {name} overlap (stride {ld} for {N} experts)")
+    torch = _torch()
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    return (BFMOE_BF16 if t.dtype == torch.bfloat16 else BFMOE_F32), T, N, ld
+
+
+def bfmoe_route_workspace_size(n_experts: int, T: int, k: int) -> int:
+    return int(capi.lib().bfmoe_route_workspace_size(n_experts, T, k))
+
+
+def _route_ws(ws, N, T, k, dev):
+    if ws is None:
+        n = bfmoe_route_workspace_size(N, T, k)
+        return _torch().empty(max(n, 256), dtype=_torch().uint8, device=dev)
+    return ws
+
+
+def bfmoe_router_logits(x, w_gate, bias=None, logits=None, ws=None, stream=None):
+    """Router logits x W_g^T (+ b) alone, float32 [T][N] (bfmoe_router_logits)."""
+    torch = _torch()
+    _need(x, "x")
+    _need(w_gate, "w_gate", torch.float32)
+    if x.dim() != 2 or w_gate.dim() != 2 or x.shape[1] != w_gate.shape[1]:
+        raise ValueError("x must be [T][d] and w_gate [N][d]")
+    T, d = x.shape
+    N = w_gate.shape[0]
+    _need_shape(bias, "bias", torch.float32, (N,))
+    code = _dtype_code(x)
+    if logits is None:
+        logits = torch.empty((T, N), dtype=torch.float32, device=x.device)
+    _need_shape(logits, "logits", torch.float32, (T, N))
+    s = _here(stream, ("x", x), ("w_gate", w_gate), ("bias", bias), ("logits", logits), ("ws", ws))
+    if ws is None:
+        ws = workspace(d, N, T, 1, code, x.device)
+    capi.check(capi.lib().bfmoe_router_logits(_ptr(x), code, T, d, _ptr(w_gate), _ptr(bias), N, _ptr(logits),
+                                              _ptr(ws), ws.numel(), s))
+    return logits
+
+
+def bfmoe_route(logits, k: int, scoring: Scoring, balance_bias=None, ws=None, out=None, buckets: bool = True,
+                stream=None):
+    """Experts and gates from logits [T][N] (float32 or bfloat16, rows may be
+    strided).  Returns (idx [T,k] int32, gates [T,k] f32, counts [N],
+    offsets [N+1], rows [T*k]); with ``buckets=False`` the last three are None
+    and are not built."""
+    torch = _torch()
+    code, T, N, ld = _logits(logits)
+    _need_shape(balance_bias, "balance_bias", torch.float32, (N,))
+    dev = logits.device
+    if out is None:
+        i32 = dict(dtype=torch.int32, device=dev)
+        out = (torch.empty((T, k), **i32), torch.empty((T, k), dtype=torch.float32, device=dev))
+        out += (torch.empty((N,), **i32), torch.empty((N + 1,), **i32),
+                torch.empty((T * k,), **i32)) if buckets else (None, None, None)
+    else:
+        _need_shape(out[0], "idx", torch.int32, (T, k))
+        _need_shape(out[1], "gates", torch.float32, (T, k))
+        for t, name, shape in ((out[2], "counts", (N,)), (out[3], "offsets", (N + 1,)), (out[4], "rows", (T * k,))):
+            _need_shape(t, name, torch.int32, shape)
+    idx, gates, counts, offsets, rows = out
+    s = _here(stream, ("logits", logits), ("balance_bias", balance_bias), ("idx", idx), ("gates", gates),
+              ("counts", counts), ("offsets", offsets), ("rows", rows), ("ws", ws))
+    if counts is not None:
+        ws = _route_ws(ws, N, T, k, dev)
+    capi.check(capi.lib().bfmoe_route(
+        _ptr(logits), code, T, ld, N, k, ctypes.byref(scoring.c), _ptr(balance_bias), _ptr(idx), _ptr(gates),
+        _ptr(counts), _ptr(offsets), _ptr(rows), _ptr(ws), ws.numel() if ws is not None else 0, s))
+    return out
+
+
+def bfmoe_balance_loss(logits, idx, score: str = "softmax", ws=None, out=None, stream=None):
+    """The load-balance and z losses of the routing idx [T,k] of logits [T][N]:
+    (loss float32 [2], load int32 [N+1]: slots of each expert, then the rows
+    that have an expert left)."""
+    torch = _torch()
+    code, T, N, ld = _logits(logits)
+    if score not in Scoring.SCORES:
+        raise ValueError(f"score must be one of {sorted(Scoring.SCORES)}, got {score!r}")
+    if idx.dim() != 2:
+        raise ValueError("idx must be [T][k]")
+    k = idx.shape[1]
+    _need_shape(idx, "idx", torch.int32, (T, k))
+    if out is None:
+        out = (torch.empty((2,), dtype=torch.float32, device=logits.device),
+               torch.empty((N + 1,), dtype=torch.int32, device=logits.device))
+    loss, load = out
+    _need_shape(loss, "loss", torch.float32, (2,))
+    _need_shape(load, "load", torch.int32, (N + 1,))
+    s = _here(stream, ("logits", logits), ("idx", idx), ("loss", loss), ("load", load), ("ws", ws))
+    ws = _route_ws(ws, N, T, k, logits.device)
+    capi.check(capi.lib().bfmoe_balance_loss(_ptr(logits), code, T, ld, N, k, Scoring.SCORES[score], _ptr(idx),
+                                             _ptr(loss), _ptr(load), _ptr(ws), ws.numel(), s))
+    return out
+
+
+def bfmoe_route_backward(logits, idx, scoring: Scoring, dgates=None, load=None, dloss=None, dlogits=None,
+                         stream=None):
+    """Gradient of the logits [T][N] (their dtype) from ``dgates`` [T,k], the
+    gradient of bfmoe_route's gates, and from ``dloss`` [2], that of
+    bfmoe_balance_loss's losses, with its ``load``."""
+    torch = _torch()
+    code, T, N, ld = _logits(logits)
+    if idx.dim() != 2:
+        raise ValueError("idx must be [T][k]")
+    k = idx.shape[1]
+    _need_shape(idx, "idx", torch.int32, (T, k))
+    _need_shape(dgates, "dgates", torch.float32, (T, k))
+    _need_shape(load, "load", torch.int32, (N + 1,))
+    _need_shape(dloss, "dloss", torch.float32, (2,))
+    if dlogits is None:
+        dlogits = torch.empty((T, N), dtype=logits.dtype, device=logits.device)
+    if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape:
+        raise ValueError("dlogits must match logits in shape and dtype")
+    ldd = _logits(dlogits, "dlogits")[3]
+    s = _here(stream, ("logits", logits), ("idx", idx), ("dgates", dgates), ("load", load), ("dloss", dloss),
+              ("dlogits", dlogits))
+    capi.check(capi.lib().bfmoe_route_backward(
+        _ptr(logits), code, T, ld, N, k, ctypes.byref(scoring.c), _ptr(idx), _ptr(dgates), _ptr(load), _ptr(dloss),
+        _ptr(dlogits), ldd, s))
+    return dlogits
+
+
+def bfmoe_expert_backward(layer: "Layer", x, k: int, routing, gy, ws=None, stream=None):
+    """bfmoe_backward without the router: float32 dx (the experts' part),
+    dtheta, dphi, dw_base, dalpha and dgates [T,k], the gradient of the gates
+    for bfmoe_route_backward."""
+    torch = _torch()
+    _need(x, "x")
+    T, d = x.shape
+    N = layer.n_experts
+    if d != layer.d:
+        raise ValueError(f"x has width {d}, layer has d={layer.d}")
+    idx, gates, _counts, offsets, rows = routing
+    _need_shape(gy, "gy", torch.float32, (T, d))
+    _need_shape(idx, "idx", torch.int32, (T, k))
+    _need_shape(gates, "gates", torch.float32, (T, k))
+    for t, name, n in ((offsets, "offsets", N + 1), (rows, "rows", T * k)):
+        if t is None:
+            raise ValueError(f"{name} is required")
+        _need_shape(t, name, torch.int32, (n,))
+    s = _here(stream, ("x", x), ("gy", gy), ("idx", idx), ("gates", gates), ("offsets", offsets), ("rows", rows),
+              ("theta", layer.theta), ("ws", ws))
+    if ws is None:
+        ws = torch.empty(max(bfmoe_backward_workspace_size(d, N, T, k), 256), dtype=torch.uint8, device=x.device)
+    f = dict(dtype=torch.float32, device=x.device)
+    out = {"dx": torch.empty((T, d), **f), "dtheta": torch.empty_like(layer.theta),
+           "dphi": torch.empty_like(layer.phi), "dw_base": torch.empty((d, d), **f),
+           "dalpha": torch.empty((1,), **f), "dgates": torch.empty((T, k), **f)}
+    capi.check(capi.lib().bfmoe_expert_backward(
+        ctypes.byref(layer.c), _ptr(x), _dtype_code(x), T, k, _ptr(idx), _ptr(gates), _ptr(offsets), _ptr(rows),
+        _ptr(gy), _ptr(out["dx"]), _ptr(out["dtheta"]), _ptr(out["dphi"]), _ptr(out["dw_base"]), _ptr(out["dalpha"]),
+        _ptr(out["dgates"]), _ptr(ws), ws.numel(), s))
+    return out
+
+
+def bfmoe_grad_workspace_size() -> int:
+    return int(capi.lib().bfmoe_grad_workspace_size())
+
+
+class GradList:
+    """A list of gradients (float32 or bfloat16, contiguous) for bfmoe_grad_norm
+    and bfmoe_grad_clip, with its workspace: made once, used every step while
+    the tensors stay where they are.  ``out``: tensors of the same shapes that
+    bfmoe_grad_clip writes instead of scaling in place (None entries: in place).
+    Calls that overlap on the GPU need a list each (they share its workspace)."""
+
+    def __init__(self, grads, out=None):
+        torch = _torch()
+        self.grads = list(grads)
+        self.out = list(out) if out is not None else [None] * len(self.grads)
+        if len(self.out) != len(self.grads):
+            raise ValueError(f"{len(self.out)} outputs for {len(self.grads)} gradients")
+        codes = {torch.float32: BFMOE_F32, torch.bfloat16: BFMOE_BF16}
+        n = len(self.grads)
+        self.c = (capi.BfmoeGrad * max(n, 1))()
+        dev = self.grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
+        for i, (g, o) in enumerate(zip(self.grads, self.out)):
+            for t, name in ((g, f"gradient {i}"), (o, f"output {i}")):
+                if t is None:
+                    continue
+                _need(t, name)
+                if t.dtype not in codes:
+                    raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+                if t.device != dev:
+                    raise ValueError(f"{name} is on {t.device}, gradient 0 on {dev}")
+                if t.shape != g.shape:
+                    raise ValueError(f"{name} has shape {tuple(t.shape)}, its gradient {tuple(g.shape)}")
+            self.c[i] = capi.BfmoeGrad(g.data_ptr(), o.data_ptr() if o is not None else None, g.numel(),
+                                       codes[g.dtype], codes[o.dtype] if o is not None else codes[g.dtype])
+        self.n = n
+        self.device = dev
+        self.ws = torch.empty(bfmoe_grad_workspace_size(), dtype=torch.uint8, device=dev)
+
+
+def _grad_list(grads):
+    g = grads if isinstance(grads, GradList) else GradList(grads)
+    dev = _torch().cuda.current_device()
+    if g.device.index != dev:
+        raise ValueError(f"the gradients are on {g.device}, the current device is cuda:{dev}")
+    return g
+
+
+def bfmoe_grad_norm(grads, norm=None, stream=None):
+    """The global norm (float32 [1]) of a GradList or of a sequence of tensors."""
+    torch = _torch()
+    g = _grad_list(grads)
+    if norm is None:
+        norm = torch.empty((1,), dtype=torch.float32, device=g.device)
+    _need_shape(norm, "norm", torch.float32, (1,))
+    s = _here(stream, ("norm", norm))
+    capi.check(capi.lib().bfmoe_grad_norm(g.c, g.n, _ptr(norm), _ptr(g.ws), g.ws.numel(), s))
+    return norm
+
+
+def bfmoe_grad_clip(grads, max_norm: float, norm=None, stream=None):
+    """Scale a GradList (or a sequence of tensors, in place) by
+    min(1, max_norm / norm); returns the norm before it (float32 [1]).  A norm
+    that is not finite leaves the gradients as they are."""
+    torch = _torch()
+    g = _grad_list(grads)
+    if norm is None:
+        norm = torch.empty((1,), dtype=torch.float32, device=g.device)
+    _need_shape(norm, "norm", torch.float32, (1,))
+    s = _here(stream, ("norm", norm))
+    capi.check(capi.lib().bfmoe_grad_clip(g.c, g.n, max_norm, _ptr(norm), _ptr(g.ws), g.ws.numel(), s))
+    return norm
+
+
 def bfmoe_materialize_expert(layer: Layer, e: int, out=None, stream=None):
     """alpha * B(phi_e) . W_base . B(theta_e)^T as float32 [d][d] (checking aid)."""
     torch = _torch()
@@ -413,11 +702,20 @@ class ButterflyMoE:
 
     ``__call__(x)`` runs on device tensors; ``forward_host(x_host, y_host)``
     is the end-to-end call: pinned host tokens in, pinned host outputs back.
+
+    With ``scoring`` the experts and gates come from bfmoe_route (on the logits
+    x W_g^T + bias, ranked with ``balance_bias``) instead of the plain softmax
+    router; the logits of the last call are in ``logits[:T]``.  forward_host
+    then has no form.
     """
 
-    def __init__(self, layer: Layer, w_gate, bias, k: int, max_tokens: int, x_dtype):
+    def __init__(self, layer: Layer, w_gate, bias, k: int, max_tokens: int, x_dtype,
+                 scoring: Optional[Scoring] = None, balance_bias=None):
         torch = _torch()
+        if balance_bias is not None and scoring is None:
+            raise ValueError("balance_bias needs a scoring")
         self.layer, self.w_gate, self.bias, self.k = layer, w_gate, bias, k
+        self.scoring, self.balance_bias = scoring, balance_bias
         self.dtype = x_dtype
         code = BFMOE_BF16 if x_dtype == torch.bfloat16 else BFMOE_F32
         dev = layer.theta.device
@@ -432,9 +730,26 @@ class ButterflyMoE:
         self.offsets = torch.empty((N + 1,), dtype=torch.int32, device=dev)
         self.rows = torch.empty((max_tokens * k,), dtype=torch.int32, device=dev)
         self.y_dev = torch.empty((max_tokens, d), dtype=x_dtype, device=dev)
+        if scoring is not None:
+            self.logits = torch.empty((max_tokens, N), dtype=torch.float32, device=dev)
+            # the logits' and the routing's scratch, one after the other
+            n = max(bfmoe_workspace_size(d, N, max_tokens, 1, code), bfmoe_route_workspace_size(N, max_tokens, k))
+            self.ws_route = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+
+    def _scored(self, x, out, stream):
+        T = x.shape[0]
+        if T > self.max_tokens:
+            raise ValueError("more tokens than the buffers hold")
+        logits = bfmoe_router_logits(x, self.w_gate, self.bias, logits=self.logits[:T], ws=self.ws_route,
+                                     stream=stream)
+        return bfmoe_route(logits, self.k, self.scoring, balance_bias=self.balance_bias, ws=self.ws_route, out=out,
+                           stream=stream)
 
     def route(self, x, stream=None):
         T = x.shape[0]
+        if self.scoring is not None:
+            return self._scored(x, (self.idx[:T], self.gates[:T], self.counts, self.offsets, self.rows[:T * self.k]),
+                                stream)
         out = (self.idx[:T], self.gates[:T], self.counts, self.offsets, self.rows[:T * self.k])
         return bfmoe_router_topk(x, self.w_gate, self.bias, self.k, self.ws, out=out, stream=stream)
 
@@ -445,6 +760,9 @@ class ButterflyMoE:
             raise ValueError("more tokens than the buffers hold")
         if y is None:
             y = self.y_dev[:T]
+        if self.scoring is not None:
+            idx, gates, _, offsets, rows = self.route(x, stream=stream)
+            return bfmoe_forward(self.layer, x, self.k, idx, gates, offsets, rows, self.ws, y=y, stream=stream)
         routing = (self.idx[:T], self.gates[:T], self.counts, self.offsets, self.rows[:T * self.k])
         y, _ = bfmoe_moe_forward(self.layer, x, self.w_gate, self.bias, self.k, self.ws_moe, routing=routing, y=y,
                                  stream=stream)
@@ -459,6 +777,9 @@ class ButterflyMoE:
         if y is None:
             y = self.y_dev[:T]
         idx, gates = self.idx[:T], self.gates[:T]
+        if self.scoring is not None:
+            self._scored(x, (idx, gates, None, None, None), stream)
+            return bfmoe_decode_forward(self.layer, x, self.k, idx, gates, y=y, stream=stream)
         bfmoe_router_topk(x, self.w_gate, self.bias, self.k, self.ws, out=(idx, gates, None, None, None),
                           stream=stream)
         return bfmoe_decode_forward(self.layer, x, self.k, idx, gates, y=y, stream=stream)
@@ -468,6 +789,8 @@ class ButterflyMoE:
         through bfmoe_moe_forward_host (copies overlapped with the work in
         token chunks).  Synchronise ``stream`` before reading y_host."""
         torch = _torch()
+        if self.scoring is not None:
+            raise ValueError("forward_host routes by the plain softmax router only")
         T = x_host.shape[0]
         key = (T, chunk)
         if getattr(self, "_host_key", None) != key:

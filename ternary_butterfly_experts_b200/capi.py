@@ -23,6 +23,10 @@ BFMOE_EDEVICE_TIMEOUT = 6
 BFMOE_EDEVICE_BOUNDS = 7
 BFMOE_F32 = 0
 BFMOE_BF16 = 1
+BFMOE_SCORE_SOFTMAX = 0
+BFMOE_SCORE_SIGMOID = 1
+BFMOE_GROUP_MAX = 0
+BFMOE_GROUP_TOP2 = 1
 BFMOE_NOALLOC_SCRATCH_BYTES = 32 << 20
 
 STATUS_NAMES = {0: "OK", 1: "EINVAL", 2: "ENOT_TERNARY", 3: "EUNSUPPORTED", 4: "EWORKSPACE",
@@ -33,6 +37,16 @@ class BfmoeLayer(ctypes.Structure):
     _fields_ = [("d", ctypes.c_int), ("n_experts", ctypes.c_int), ("w_packed", ctypes.c_void_p),
                 ("alpha", ctypes.c_float), ("theta", ctypes.c_void_p), ("phi", ctypes.c_void_p),
                 ("tables", ctypes.c_void_p), ("gate_parts", ctypes.c_void_p)]
+
+
+class BfmoeScoring(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int), ("n_groups", ctypes.c_int), ("top_groups", ctypes.c_int),
+                ("group_score", ctypes.c_int), ("renormalize", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class BfmoeGrad(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("len", ctypes.c_longlong),
+                ("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int)]
 
 
 class BfmoeKernelTime(ctypes.Structure):
@@ -49,7 +63,10 @@ _lib = None
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_LL = ctypes.c_longlong
 _SZ = ctypes.c_size_t
+_SCORING = ctypes.POINTER(BfmoeScoring)
+_GRADS = ctypes.POINTER(BfmoeGrad)
 
 SIGNATURES = {
     "bfmoe_pack_base": (_I, [_P, _I, _P, _P]),
@@ -69,6 +86,16 @@ SIGNATURES = {
     "bfmoe_moe_host_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "bfmoe_materialize_expert": (_I, [ctypes.POINTER(BfmoeLayer), _I, _P, _P]),
     "bfmoe_decode_forward": (_I, [ctypes.POINTER(BfmoeLayer), _P, _I, _I, _I, _P, _P, _P, _P]),
+    "bfmoe_router_logits": (_I, [_P, _I, _I, _I, _P, _P, _I, _P, _P, _SZ, _P]),
+    "bfmoe_route": (_I, [_P, _I, _I, _LL, _I, _I, _SCORING, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "bfmoe_balance_loss": (_I, [_P, _I, _I, _LL, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
+    "bfmoe_route_backward": (_I, [_P, _I, _I, _LL, _I, _I, _SCORING, _P, _P, _P, _P, _P, _LL, _P]),
+    "bfmoe_route_workspace_size": (_SZ, [_I, _I, _I]),
+    "bfmoe_expert_backward": (_I, [ctypes.POINTER(BfmoeLayer), _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                   _P, _P, _SZ, _P]),
+    "bfmoe_grad_norm": (_I, [_GRADS, _I, _P, _P, _SZ, _P]),
+    "bfmoe_grad_clip": (_I, [_GRADS, _I, ctypes.c_float, _P, _P, _SZ, _P]),
+    "bfmoe_grad_workspace_size": (_SZ, []),
     "bfmoe_prepare_gate": (_I, [_P, _I, _I, _P, _SZ, _P]),
     "bfmoe_gate_parts_size": (_SZ, [_I, _I]),
     "bfmoe_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),

@@ -363,7 +363,7 @@ __global__ void sum_kernel(const float* __restrict__ part, int n, float* __restr
 
 // Per token: dl_j = g_j (dg_j - sum_j' g_j' dg_j'), then
 // dx_t = sum_j (dXr[t k + j] + dl_j W_g[e_j]) in slot order.  One warp per
-// token.
+// token.  Without w_gate the router is left out: dx_t = sum_j dXr[t k + j].
 template <typename Tx>
 __global__ __launch_bounds__(256) void bw_token_kernel(const float* __restrict__ dXr, const float* __restrict__ dg,
                                                        const float* __restrict__ gates,
@@ -373,6 +373,14 @@ __global__ __launch_bounds__(256) void bw_token_kernel(const float* __restrict__
   const int lane = threadIdx.x & 31;
   const long long nwarps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
   for (long long t = (blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x) >> 5; t < T; t += nwarps) {
+    if (!w_gate) {
+      for (int c = lane; c < d; c += 32) {
+        float s = 0.f;
+        for (int j = 0; j < k; ++j) s += dXr[(t * k + j) * d + c];
+        dx[t * d + c] = s;
+      }
+      continue;
+    }
     float gd = 0.f;
     for (int j = 0; j < k; ++j) gd += gates[t * k + j] * dg[t * k + j];
     float dlj[BFMOE_MAX_K];

@@ -20,6 +20,7 @@
 #include "fused_tc.cuh"
 #include "gemm_simt.cuh"
 #include "gemm_tc.cuh"
+#include "host.cuh"
 #include "materialize.cuh"
 #include "pack.cuh"
 #include "rotate.cuh"
@@ -30,136 +31,6 @@
 using namespace bfmoe;
 
 namespace {
-
-thread_local char g_last_error[512] = "";
-
-int fail(int code, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
-  va_end(ap);
-  return code;
-}
-int ok() {
-  g_last_error[0] = '\0';
-  return BFMOE_OK;
-}
-int cuda_fail(cudaError_t e, const char* what) {
-  return fail(BFMOE_ECUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-bool is_pow2(long long v) { return v > 0 && (v & (v - 1)) == 0; }
-int ilog2(int v) {
-  int l = 0;
-  while ((1 << l) < v) ++l;
-  return l;
-}
-size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-int words_per_row(int d) { return std::max(1, (d + 15) / 16); }
-
-// ---------------------------------------------------------------------------
-// Launch accounting and optional per-launch CUDA events.
-// ---------------------------------------------------------------------------
-std::atomic<unsigned long long> g_launches{0};
-std::mutex g_prof_mu;
-bool g_prof_on = false;
-struct ProfRec {
-  const char* name;
-  cudaEvent_t a, b;
-};
-std::vector<ProfRec> g_prof;
-std::vector<cudaEvent_t> g_event_pool;
-
-cudaEvent_t pool_event() {
-  if (!g_event_pool.empty()) {
-    cudaEvent_t e = g_event_pool.back();
-    g_event_pool.pop_back();
-    return e;
-  }
-  cudaEvent_t e = nullptr;
-  cudaEventCreate(&e);
-  return e;
-}
-
-template <typename F>
-cudaError_t launch(const char* name, cudaStream_t s, F&& f) {
-  ProfRec rec{name, nullptr, nullptr};
-  bool prof;
-  {
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    prof = g_prof_on;
-    if (prof) {
-      rec.a = pool_event();
-      rec.b = pool_event();
-    }
-  }
-  if (prof) cudaEventRecord(rec.a, s);
-  f();
-  const cudaError_t e = cudaGetLastError();
-  if (prof) {
-    cudaEventRecord(rec.b, s);
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    g_prof.push_back(rec);
-  }
-  g_launches.fetch_add(1, std::memory_order_relaxed);
-  return e;
-}
-
-// Launch with programmatic stream serialisation: the kernel may start while
-// the previous kernel of the stream finishes; it waits for that kernel's
-// results with pdl_wait() before touching global memory.
-template <typename... KP, typename... A>
-void pdl_launch(void (*kern)(KP...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A&&... args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...);
-}
-
-// Kernel attributes (dynamic shared-memory limits) are set per device: the
-// first launch of a kernel on each device sets them.  `done` holds one bit
-// per device and is set only after the attribute, so concurrent first calls
-// both set it (the call is idempotent).
-int current_device() {
-  int dev = 0;
-  cudaGetDevice(&dev);
-  return dev & 63;
-}
-bool needs_attr(const std::atomic<uint64_t>& done) {
-  return (done.load(std::memory_order_acquire) >> current_device() & 1u) == 0;
-}
-void attr_set(std::atomic<uint64_t>& done) {
-  done.fetch_or(uint64_t(1) << current_device(), std::memory_order_release);
-}
-
-int grid_for(long long work, int per_block, int cap) {
-  long long g = (work + per_block - 1) / per_block;
-  if (g < 1) g = 1;
-  if (g > cap) g = cap;
-  return static_cast<int>(g);
-}
-
-// SMs of the current device (cached per device).
-int sm_count() {
-  static std::atomic<int> n[64] = {};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  dev &= 63;
-  int v = n[dev].load(std::memory_order_relaxed);
-  if (v == 0) {
-    cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
-    if (v <= 0) v = 148;
-    n[dev].store(v, std::memory_order_relaxed);
-  }
-  return v;
-}
 
 // ---------------------------------------------------------------------------
 // Workspace: router and forward share one buffer (stream-ordered).
@@ -261,11 +132,6 @@ int check_sizes(int d, int N, long long T, int k) {
   if (T * k > 0x7fffffffLL) return fail(BFMOE_EUNSUPPORTED, "T*k=%lld exceeds int32 row ids", T * k);
   return BFMOE_OK;
 }
-int check_dtype(int xdt) {
-  if (xdt != BFMOE_F32 && xdt != BFMOE_BF16) return fail(BFMOE_EINVAL, "x_dtype=%d is not BFMOE_F32 or BFMOE_BF16", xdt);
-  return BFMOE_OK;
-}
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int check_ws(const Plan& p, void* ws, size_t ws_bytes, size_t need) {
   if (need == 0) return BFMOE_OK;
@@ -952,6 +818,36 @@ cudaError_t bw_rows_dispatch(int d, const void* x, bool bf16, const int32_t* idx
 
 }  // namespace
 
+namespace bfmoe {
+
+cudaError_t build_buckets(const int32_t* idx, long long R, int k, int N, bool have_histograms, int32_t* cc,
+                          int32_t* totals, int32_t* counts, int32_t* offsets, int32_t* rows, int32_t* pad_out,
+                          long long p_cap, cudaStream_t s) {
+  const int chunk = bucket_chunk(k);
+  const int nchunks = static_cast<int>((R + chunk - 1) / chunk);
+  static std::atomic<uint64_t> done{0};
+  if (needs_attr(done)) {
+    cudaFuncSetAttribute(bucket_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BFMOE_MAX_EXPERTS * 4);
+    cudaFuncSetAttribute(bucket_scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         BFMOE_MAX_EXPERTS * 40 + 32);
+    attr_set(done);
+  }
+  cudaError_t e = cudaSuccess;
+  if (!have_histograms) {
+    e = launch("bucket_count", s, [&] { bucket_count_kernel<<<nchunks, chunk, N * 4, s>>>(idx, R, N, cc); });
+    if (e != cudaSuccess) return e;
+  }
+  e = launch("bucket_scan", s, [&] { pdl_launch(bucket_scan_kernel, (N + 31) / 32, 1024, 0, s, cc, nchunks, N, totals); });
+  if (e != cudaSuccess) return e;
+  const size_t scatter_smem = ((N + 1) * 4 + 15) / 16 * 16 + static_cast<size_t>(N) * 36 + 4;
+  return launch("bucket_scatter", s, [&] {
+    pdl_launch(bucket_scatter_kernel, nchunks, chunk, scatter_smem, s, idx, R, N, static_cast<const int32_t*>(cc),
+               static_cast<const int32_t*>(totals), counts, offsets, rows, pad_out, p_cap);
+  });
+}
+
+}  // namespace bfmoe
+
 // ===========================================================================
 // C ABI
 // ===========================================================================
@@ -1030,6 +926,29 @@ int bfmoe_router_topk(const void* x, int x_dtype, int T, int d, const float* w_g
 
 namespace {
 
+// The float32 error band that leaves a top-k undecided (router.cuh).
+float router_eps(int d) { return 2e-5f * std::sqrt(static_cast<float>(d) / 2048.f); }
+
+// The tensor-core router (router_tc.cuh) on split weights.
+int router_tc_any(const void* x, const __nv_bfloat16* parts, const float* bias, int T, int d, int N, int k,
+                  float* logits, const float* w_gate, int32_t* idx, float* gates, int32_t* cc, cudaStream_t s) {
+  const float eps_c = router_eps(d);
+  const int BN = N >= 128 ? 128 : (N > 32 ? 64 : (N > 16 ? 32 : 16));
+  const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(x);
+  CUtensorMap tx, tw;
+  if (!make_tmap_bf16(&tx, x, d, T, kGemmBM) || !make_tmap_bf16(&tw, parts, d, 3LL * N, BN))
+    return fail(BFMOE_ECUDA, "router: tensor map encoding failed");
+  cudaError_t e;
+  switch (BN) {
+    case 16: e = launch_router_tc<16, 4>(tx, tw, bias, T, d, N, k, eps_c, logits, xb, w_gate, idx, gates, cc, s); break;
+    case 32: e = launch_router_tc<32, 4>(tx, tw, bias, T, d, N, k, eps_c, logits, xb, w_gate, idx, gates, cc, s); break;
+    case 64: e = launch_router_tc<64, 4>(tx, tw, bias, T, d, N, k, eps_c, logits, xb, w_gate, idx, gates, cc, s); break;
+    default: e = launch_router_tc<128, 3>(tx, tw, bias, T, d, N, k, eps_c, logits, xb, w_gate, idx, gates, cc, s); break;
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "router: tensor-core kernel");
+  return ok();
+}
+
 int router_topk_impl(const void* x, int x_dtype, int T, int d, const float* w_gate, const float* bias, int n_experts,
                      int k, int32_t* idx, float* gates, int32_t* counts, int32_t* offsets, int32_t* rows, void* ws,
                      size_t ws_bytes, cudaStream_t s, const __nv_bfloat16* parts_ready, int32_t* pad_out) {
@@ -1058,8 +977,7 @@ int router_topk_impl(const void* x, int x_dtype, int T, int d, const float* w_ga
   int32_t* totals = reinterpret_cast<int32_t*>(W + p.totals);
   int* unsure = reinterpret_cast<int*>(W + p.unsure);
   const long long R = static_cast<long long>(T) * k;
-  // the float32 error band that leaves a top-k undecided (router.cuh)
-  const float eps_c = 2e-5f * std::sqrt(static_cast<float>(d) / 2048.f);
+  const float eps_c = router_eps(d);
   const bool tc_router = tc_router_path(x_dtype, d);
   if (!tc_router && (e = cudaMemsetAsync(unsure, 0, 8, s)) != cudaSuccess) return cuda_fail(e, "router_topk: memset");
   if (tc_router) {
@@ -1071,18 +989,7 @@ int router_topk_impl(const void* x, int x_dtype, int T, int d, const float* w_ga
       if ((e = split_gate_weights(w_gate, N, d, own, s)) != cudaSuccess) return cuda_fail(e, "router_topk: split");
       parts = own;
     }
-    const int BN = N >= 128 ? 128 : (N > 32 ? 64 : (N > 16 ? 32 : 16));
-    const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(x);
-    CUtensorMap tx, tw;
-    if (!make_tmap_bf16(&tx, x, d, T, kGemmBM) || !make_tmap_bf16(&tw, parts, d, 3LL * N, BN))
-      return fail(BFMOE_ECUDA, "router_topk: tensor map encoding failed");
-    switch (BN) {
-      case 16: e = launch_router_tc<16, 4>(tx, tw, bias, T, d, N, k, eps_c, logits, xb, w_gate, idx, gates, cc, s); break;
-      case 32: e = launch_router_tc<32, 4>(tx, tw, bias, T, d, N, k, eps_c, logits, xb, w_gate, idx, gates, cc, s); break;
-      case 64: e = launch_router_tc<64, 4>(tx, tw, bias, T, d, N, k, eps_c, logits, xb, w_gate, idx, gates, cc, s); break;
-      default: e = launch_router_tc<128, 3>(tx, tw, bias, T, d, N, k, eps_c, logits, xb, w_gate, idx, gates, cc, s); break;
-    }
-    if (e != cudaSuccess) return cuda_fail(e, "router_topk: tensor-core router");
+    if ((rc = router_tc_any(x, parts, bias, T, d, N, k, logits, w_gate, idx, gates, cc, s))) return rc;
   } else {
     dim3 g1((T + 63) / 64, (N + 63) / 64);
     e = launch("router_logits_simt", s, [&] {
@@ -1124,32 +1031,51 @@ int router_topk_impl(const void* x, int x_dtype, int T, int d, const float* w_ga
     if (e != cudaSuccess) return cuda_fail(e, "router_topk: fix-up of undecided tokens");
   }
 
-  const int chunk = bucket_chunk(k);
   if (!buckets) return ok();
-  const int nchunks = static_cast<int>((R + chunk - 1) / chunk);
-  static std::atomic<uint64_t> done{0};
-  if (needs_attr(done)) {
-    cudaFuncSetAttribute(bucket_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BFMOE_MAX_EXPERTS * 4);
-    cudaFuncSetAttribute(bucket_scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         BFMOE_MAX_EXPERTS * 40 + 32);
-    attr_set(done);
-  }
-  if (!tc_router) {  // the tensor-core router writes the chunk histograms itself
-    e = launch("bucket_count", s, [&] { bucket_count_kernel<<<nchunks, chunk, N * 4, s>>>(idx, R, N, cc); });
-    if (e != cudaSuccess) return cuda_fail(e, "router_topk: bucket count");
-  }
-  e = launch("bucket_scan", s, [&] { pdl_launch(bucket_scan_kernel, (N + 31) / 32, 1024, 0, s, cc, nchunks, N, totals); });
-  if (e != cudaSuccess) return cuda_fail(e, "router_topk: bucket scan");
-  const size_t scatter_smem = ((N + 1) * 4 + 15) / 16 * 16 + static_cast<size_t>(N) * 36 + 4;
-  e = launch("bucket_scatter", s, [&] {
-    pdl_launch(bucket_scatter_kernel, nchunks, chunk, scatter_smem, s, idx, R, N, static_cast<const int32_t*>(cc),
-               static_cast<const int32_t*>(totals), counts, offsets, rows, pad_out, pad_cap(R, N));
-  });
-  if (e != cudaSuccess) return cuda_fail(e, "router_topk: bucket scatter");
+  // the tensor-core router writes the chunk histograms itself
+  e = build_buckets(idx, R, k, N, tc_router, cc, totals, counts, offsets, rows, pad_out, pad_cap(R, N), s);
+  if (e != cudaSuccess) return cuda_fail(e, "router_topk: buckets");
   return ok();
 }
 
 }  // namespace
+
+int bfmoe_router_logits(const void* x, int x_dtype, int T, int d, const float* w_gate, const float* bias,
+                        int n_experts, float* logits, void* ws, size_t ws_bytes, bfmoe_stream_t stream) {
+  const int N = n_experts;
+  int rc = check_sizes(d, N, T, 1);
+  if (rc) return rc;
+  if ((rc = check_dtype(x_dtype))) return rc;
+  if (T == 0) return ok();
+  if (!x || !w_gate || !logits) return fail(BFMOE_EINVAL, "router_logits: NULL pointer");
+  if (reinterpret_cast<uintptr_t>(logits) & 31u) return fail(BFMOE_EINVAL, "router_logits: logits must be 32-byte aligned");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (!tc_router_path(x_dtype, d)) {
+    dim3 g1((T + 63) / 64, (N + 63) / 64);
+    e = launch("router_logits_simt", s, [&] {
+      if (x_dtype == BFMOE_BF16)
+        router_logits_simt_kernel<__nv_bfloat16><<<g1, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(x), w_gate,
+                                                                    bias, T, d, N, logits);
+      else
+        router_logits_simt_kernel<float><<<g1, 256, 0, s>>>(static_cast<const float*>(x), w_gate, bias, T, d, N,
+                                                            logits);
+    });
+    if (e != cudaSuccess) return cuda_fail(e, "router_logits: launch");
+    return ok();
+  }
+  // the tensor-core router with one pick a token, its logits stored in the
+  // caller's memory; the pick goes to the workspace (where the logits of
+  // bfmoe_router_topk, 4 N bytes a token, leave room for the gates)
+  if (!aligned16(x)) return fail(BFMOE_EINVAL, "router_logits: x must be 16-byte aligned");
+  const Plan p = make_plan(d, N, T, 1, x_dtype);
+  if ((rc = check_ws(p, ws, ws_bytes, p.rt_end))) return rc;
+  uint8_t* W = static_cast<uint8_t*>(ws);
+  auto* parts = reinterpret_cast<__nv_bfloat16*>(W + p.wg_parts);
+  if ((e = split_gate_weights(w_gate, N, d, parts, s)) != cudaSuccess) return cuda_fail(e, "router_logits: split");
+  return router_tc_any(x, parts, bias, T, d, N, 1, logits, w_gate, reinterpret_cast<int32_t*>(W + p.unsure),
+                       reinterpret_cast<float*>(W + p.logits), reinterpret_cast<int32_t*>(W + p.chunk_counts), s);
+}
 
 int bfmoe_router_topk_noalloc(const void* x, int x_dtype, int T, int d, const float* w_gate, const float* bias,
                               int n_experts, int k, int32_t* idx, float* gates, int32_t* counts, int32_t* offsets,
@@ -1441,19 +1367,26 @@ size_t bfmoe_backward_workspace_size(int d, int n_experts, int T, int k) {
   return make_bw_plan(d, n_experts, T, k).total;
 }
 
-int bfmoe_backward(const bfmoe_layer* layer, const void* x, int x_dtype, int T, int k, const float* w_gate,
-                   const int32_t* idx, const float* gates, const int32_t* offsets, const int32_t* rows,
-                   const float* gy, float* dx, float* dtheta, float* dphi, float* dw_base, float* dalpha,
-                   float* dw_gate, float* dbias, void* ws, size_t ws_bytes, bfmoe_stream_t stream) {
+namespace {
+
+// The body of bfmoe_backward and of bfmoe_expert_backward: with dgates the
+// router is left out (w_gate, dw_gate and dbias NULL) and the gates' gradient
+// goes there.
+int backward_impl(const bfmoe_layer* layer, const void* x, int x_dtype, int T, int k, const float* w_gate,
+                  const int32_t* idx, const float* gates, const int32_t* offsets, const int32_t* rows,
+                  const float* gy, float* dx, float* dtheta, float* dphi, float* dw_base, float* dalpha,
+                  float* dw_gate, float* dbias, float* dgates, bool router, void* ws, size_t ws_bytes,
+                  bfmoe_stream_t stream) {
   if (!layer) return fail(BFMOE_EINVAL, "backward: NULL layer");
   const int d = layer->d, N = layer->n_experts, L = ilog2(d);
   int rc = check_sizes(d, N, T, k);
   if (rc) return rc;
   if ((rc = check_dtype(x_dtype))) return rc;
   if (!layer->w_packed || !layer->theta || !layer->phi) return fail(BFMOE_EINVAL, "backward: NULL layer weights");
-  if (!dtheta || !dphi || !dw_base || !dalpha || !dw_gate || !w_gate || !offsets)
+  if (!dtheta || !dphi || !dw_base || !dalpha || (router && (!dw_gate || !w_gate)) || !offsets)
     return fail(BFMOE_EINVAL, "backward: NULL pointer");
-  if (T > 0 && (!x || !idx || !gates || !rows || !gy || !dx)) return fail(BFMOE_EINVAL, "backward: NULL pointer");
+  if (T > 0 && (!x || !idx || !gates || !rows || !gy || !dx || (!router && !dgates)))
+    return fail(BFMOE_EINVAL, "backward: NULL pointer");
   const BwPlan b = make_bw_plan(d, N, T, k);
   if (!ws) return fail(BFMOE_EWORKSPACE, "backward: NULL workspace");
   if (reinterpret_cast<uintptr_t>(ws) & 255u) return fail(BFMOE_EWORKSPACE, "backward: workspace must be 256-byte aligned");
@@ -1466,7 +1399,7 @@ int bfmoe_backward(const bfmoe_layer* layer, const void* x, int x_dtype, int T, 
   float* U = reinterpret_cast<float*>(W + b.U);
   float* Z = reinterpret_cast<float*>(W + b.Z);
   float* dU = reinterpret_cast<float*>(W + b.dU);
-  float* dg = reinterpret_cast<float*>(W + b.dg);
+  float* dg = router ? reinterpret_cast<float*>(W + b.dg) : dgates;
   float* dl = reinterpret_cast<float*>(W + b.dl);
   float* part = reinterpret_cast<float*>(W + b.part);
   float* dapart = reinterpret_cast<float*>(W + b.dapart);
@@ -1490,7 +1423,7 @@ int bfmoe_backward(const bfmoe_layer* layer, const void* x, int x_dtype, int T, 
     if ((e = cudaMemsetAsync(dtheta, 0, ang, s)) != cudaSuccess || (e = cudaMemsetAsync(dphi, 0, ang, s)) != cudaSuccess ||
         (e = cudaMemsetAsync(dw_base, 0, static_cast<size_t>(d) * d * 4, s)) != cudaSuccess ||
         (e = cudaMemsetAsync(dalpha, 0, 4, s)) != cudaSuccess ||
-        (e = cudaMemsetAsync(dw_gate, 0, static_cast<size_t>(N) * d * 4, s)) != cudaSuccess ||
+        (router && (e = cudaMemsetAsync(dw_gate, 0, static_cast<size_t>(N) * d * 4, s)) != cudaSuccess) ||
         (dbias && (e = cudaMemsetAsync(dbias, 0, static_cast<size_t>(N) * 4, s)) != cudaSuccess))
       return cuda_fail(e, "backward: memset");
     return ok();
@@ -1536,7 +1469,7 @@ int bfmoe_backward(const bfmoe_layer* layer, const void* x, int x_dtype, int T, 
     else
       bw_token_kernel<float><<<g, 256, 0, s>>>(Z, dg, gates, idx, w_gate, T, k, d, N, dl, dx);
   });
-  if (e == cudaSuccess)
+  if (e == cudaSuccess && router)
     e = launch("bw_router", s, [&] {
       if (bf16)
         bw_router_kernel<__nv_bfloat16><<<N, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(x), dl, rows, offsets, k, d,
@@ -1549,6 +1482,24 @@ int bfmoe_backward(const bfmoe_layer* layer, const void* x, int x_dtype, int T, 
   return ok();
 }
 
+}  // namespace
+
+int bfmoe_backward(const bfmoe_layer* layer, const void* x, int x_dtype, int T, int k, const float* w_gate,
+                   const int32_t* idx, const float* gates, const int32_t* offsets, const int32_t* rows,
+                   const float* gy, float* dx, float* dtheta, float* dphi, float* dw_base, float* dalpha,
+                   float* dw_gate, float* dbias, void* ws, size_t ws_bytes, bfmoe_stream_t stream) {
+  return backward_impl(layer, x, x_dtype, T, k, w_gate, idx, gates, offsets, rows, gy, dx, dtheta, dphi, dw_base,
+                       dalpha, dw_gate, dbias, nullptr, true, ws, ws_bytes, stream);
+}
+
+int bfmoe_expert_backward(const bfmoe_layer* layer, const void* x, int x_dtype, int T, int k, const int32_t* idx,
+                          const float* gates, const int32_t* offsets, const int32_t* rows, const float* gy, float* dx,
+                          float* dtheta, float* dphi, float* dw_base, float* dalpha, float* dgates, void* ws,
+                          size_t ws_bytes, bfmoe_stream_t stream) {
+  return backward_impl(layer, x, x_dtype, T, k, nullptr, idx, gates, offsets, rows, gy, dx, dtheta, dphi, dw_base,
+                       dalpha, nullptr, nullptr, dgates, false, ws, ws_bytes, stream);
+}
+
 int bfmoe_check_device_error(bfmoe_stream_t stream) {
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaStreamSynchronize(s);
@@ -1556,7 +1507,12 @@ int bfmoe_check_device_error(bfmoe_stream_t stream) {
   unsigned code = 0, info = 0;
   if ((e = cudaMemcpyFromSymbol(&code, g_err_code, sizeof(code))) != cudaSuccess) return cuda_fail(e, "read error word");
   if ((e = cudaMemcpyFromSymbol(&info, g_err_info, sizeof(info))) != cudaSuccess) return cuda_fail(e, "read error word");
-  if (code == 0) return ok();
+  if (code == 0) {
+    // the other translation unit's kernels record in its own word
+    if ((e = take_route_error(&code, &info)) != cudaSuccess) return cuda_fail(e, "read error word");
+    if (code == 0) return ok();
+    return fail(static_cast<int>(code), "device check failed (code %u, at %u)", code, info);
+  }
   const unsigned zero = 0;
   cudaMemcpyToSymbol(g_err_code, &zero, sizeof(zero));
   cudaMemcpyToSymbol(g_err_info, &zero, sizeof(zero));

@@ -1,0 +1,382 @@
+// Host side of routing from logits, its gradient, the balance losses and the
+// gradient norm (include/bfmoe.h): argument checks, workspace layout, launches.
+#include <algorithm>
+#include <cmath>
+#include <new>
+#include <vector>
+
+#include "common.cuh"
+#include "grad_clip.cuh"
+#include "host.cuh"
+#include "route.cuh"
+#include "route_grad.cuh"
+
+namespace bfmoe {
+
+cudaError_t take_route_error(unsigned* code, unsigned* info) {
+  cudaError_t e = cudaMemcpyFromSymbol(code, g_err_code, sizeof(*code));
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(info, g_err_info, sizeof(*info));
+  if (e != cudaSuccess || *code == 0) return e;
+  const unsigned zero = 0;
+  e = cudaMemcpyToSymbol(g_err_code, &zero, sizeof(zero));
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_err_info, &zero, sizeof(zero));
+  return e;
+}
+
+}  // namespace bfmoe
+
+using namespace bfmoe;
+
+namespace {
+
+// Blocks of the loss kernel, which leaves one row of partial sums each.
+constexpr int kBalanceBlocks = 296;
+
+struct RoutePlan {
+  size_t chunk_counts, totals;  // buckets
+  size_t part, zpart;           // balance loss
+  size_t total;
+};
+
+RoutePlan make_route_plan(int N, long long T, int k) {
+  RoutePlan p{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += align_up(bytes, 256);
+    return o;
+  };
+  const long long nchunks = std::max(1LL, (T + 127) / 128);
+  (void)k;
+  p.chunk_counts = take(static_cast<size_t>(nchunks) * N * 4);
+  p.totals = take(static_cast<size_t>(N) * 4);
+  const size_t buckets_end = off;
+  off = 0;
+  p.part = take(static_cast<size_t>(kBalanceBlocks) * N * 4);
+  p.zpart = take(static_cast<size_t>(kBalanceBlocks) * 8);
+  p.total = std::max(buckets_end, off);
+  return p;
+}
+
+int check_routing_sizes(const char* what, int N, long long T, int k, long long ld, int dtype) {
+  if (N < 1 || N > BFMOE_MAX_EXPERTS) return fail(BFMOE_EINVAL, "%s: n_experts=%d must be in [1, %d]", what, N, BFMOE_MAX_EXPERTS);
+  if (k < 1 || k > BFMOE_MAX_K || k > N) return fail(BFMOE_EINVAL, "%s: k=%d must be in [1, min(%d, N=%d)]", what, k, BFMOE_MAX_K, N);
+  if (T < 0) return fail(BFMOE_EINVAL, "%s: T=%lld must be >= 0", what, T);
+  if (T * k > 0x7fffffffLL) return fail(BFMOE_EUNSUPPORTED, "%s: T*k=%lld exceeds int32 row ids", what, T * k);
+  if (ld < N) return fail(BFMOE_EINVAL, "%s: row stride %lld is less than n_experts=%d", what, ld, N);
+  if (dtype != BFMOE_F32 && dtype != BFMOE_BF16) return fail(BFMOE_EINVAL, "%s: dtype=%d is not BFMOE_F32 or BFMOE_BF16", what, dtype);
+  return BFMOE_OK;
+}
+
+int check_scoring(const char* what, const bfmoe_scoring* s, int N, int k) {
+  if (!s) return fail(BFMOE_EINVAL, "%s: NULL scoring", what);
+  if (s->score != BFMOE_SCORE_SOFTMAX && s->score != BFMOE_SCORE_SIGMOID)
+    return fail(BFMOE_EINVAL, "%s: score=%d is not softmax or sigmoid", what, s->score);
+  if (s->group_score != BFMOE_GROUP_MAX && s->group_score != BFMOE_GROUP_TOP2)
+    return fail(BFMOE_EINVAL, "%s: group_score=%d is not max or top2", what, s->group_score);
+  if (s->n_groups < 1 || s->n_groups > BFMOE_MAX_GROUPS || N % s->n_groups != 0)
+    return fail(BFMOE_EINVAL, "%s: n_groups=%d must divide n_experts=%d and be in [1, %d]", what, s->n_groups, N,
+                BFMOE_MAX_GROUPS);
+  if (s->top_groups < 1 || s->top_groups > s->n_groups)
+    return fail(BFMOE_EINVAL, "%s: top_groups=%d must be in [1, n_groups=%d]", what, s->top_groups, s->n_groups);
+  if (k > s->top_groups * (N / s->n_groups))
+    return fail(BFMOE_EINVAL, "%s: k=%d exceeds the %d experts of the kept groups", what, k,
+                s->top_groups * (N / s->n_groups));
+  if (!std::isfinite(s->scale)) return fail(BFMOE_EINVAL, "%s: scale must be finite", what);
+  return BFMOE_OK;
+}
+
+RouteCfg cfg_of(const bfmoe_scoring* s) {
+  return RouteCfg{s->score, s->n_groups, s->top_groups, s->group_score, s->renormalize ? 1 : 0, s->scale};
+}
+
+int check_elem_align(const char* what, const char* name, const void* p, int dtype) {
+  if (reinterpret_cast<uintptr_t>(p) & (dtype == BFMOE_BF16 ? 1u : 3u))
+    return fail(BFMOE_EINVAL, "%s: %s must be aligned to its elements", what, name);
+  return BFMOE_OK;
+}
+
+int check_space(const char* what, void* ws, size_t have, size_t need) {
+  if (!ws) return fail(BFMOE_EWORKSPACE, "%s: workspace is NULL (%zu bytes needed)", what, need);
+  if (reinterpret_cast<uintptr_t>(ws) & 255u) return fail(BFMOE_EWORKSPACE, "%s: workspace must be 256-byte aligned", what);
+  if (have < need) return fail(BFMOE_EWORKSPACE, "%s: workspace has %zu bytes, %zu needed", what, have, need);
+  return BFMOE_OK;
+}
+
+size_t type_size(int dtype) { return dtype == BFMOE_BF16 ? 2 : 4; }
+
+int check_grads(const char* what, const bfmoe_grad* g, int n, bool with_out) {
+  if (n < 0 || (n > 0 && !g)) return fail(BFMOE_EINVAL, "%s: n=%d tensors at %p", what, n, static_cast<const void*>(g));
+  if (n > kGradsPerLaunch * 64) return fail(BFMOE_EUNSUPPORTED, "%s: more than %d tensors", what, kGradsPerLaunch * 64);
+  for (int i = 0; i < n; ++i) {
+    int rc;
+    if (g[i].len < 0) return fail(BFMOE_EINVAL, "%s: tensor %d has length %lld", what, i, g[i].len);
+    if ((g[i].dtype != BFMOE_F32 && g[i].dtype != BFMOE_BF16) ||
+        (with_out && g[i].out && g[i].out_dtype != BFMOE_F32 && g[i].out_dtype != BFMOE_BF16))
+      return fail(BFMOE_EINVAL, "%s: tensor %d is not BFMOE_F32 or BFMOE_BF16", what, i);
+    if (g[i].len == 0) continue;
+    if (!g[i].grad) return fail(BFMOE_EINVAL, "%s: tensor %d is NULL", what, i);
+    if ((rc = check_elem_align(what, "a gradient", g[i].grad, g[i].dtype))) return rc;
+    if (with_out && g[i].out) {
+      if ((rc = check_elem_align(what, "an output", g[i].out, g[i].out_dtype))) return rc;
+      if (g[i].out == g[i].grad && g[i].out_dtype != g[i].dtype)
+        return fail(BFMOE_EINVAL, "%s: tensor %d is scaled in place into another type", what, i);
+    }
+  }
+  return BFMOE_OK;
+}
+
+// What a clip writes may overlap nothing else of the list (a tensor scaled in
+// place overlaps itself): an element must be read before it is written, once.
+int check_overlap(const char* what, const bfmoe_grad* g, int n) {
+  struct Span {
+    uintptr_t a, b;
+    int i;
+    bool written;
+  };
+  try {
+    std::vector<Span> v;
+    v.reserve(static_cast<size_t>(n) * 2);
+    for (int i = 0; i < n; ++i) {
+      if (g[i].len == 0) continue;
+      const uintptr_t a = reinterpret_cast<uintptr_t>(g[i].grad);
+      const bool in_place = !g[i].out || g[i].out == g[i].grad;
+      v.push_back({a, a + static_cast<size_t>(g[i].len) * type_size(g[i].dtype), i, in_place});
+      if (!in_place) {
+        const uintptr_t o = reinterpret_cast<uintptr_t>(g[i].out);
+        v.push_back({o, o + static_cast<size_t>(g[i].len) * type_size(g[i].out_dtype), i, true});
+      }
+    }
+    std::sort(v.begin(), v.end(), [](const Span& x, const Span& y) { return x.a < y.a; });
+    uintptr_t end = 0, end_written = 0;  // of all spans so far, of the written ones
+    for (const Span& s : v) {
+      if (s.a < end_written || (s.written && s.a < end))
+        return fail(BFMOE_EINVAL, "%s: tensor %d overlaps memory that the call writes", what, s.i);
+      end = std::max(end, s.b);
+      if (s.written) end_written = std::max(end_written, s.b);
+    }
+  } catch (const std::bad_alloc&) {
+    return fail(BFMOE_EINVAL, "%s: out of host memory for %d tensors", what, n);
+  }
+  return BFMOE_OK;
+}
+
+// Tensors [i0, i1) of the list as a kernel argument; empty ones are left out.
+void fill_list(const bfmoe_grad* g, int i0, int i1, GradList& out) {
+  out.n = 0;
+  long long chunks = 0;
+  for (int i = i0; i < i1; ++i) {
+    if (g[i].len == 0) continue;
+    const int q = out.n++;
+    out.src[q] = g[i].grad;
+    out.dst[q] = g[i].out ? g[i].out : const_cast<void*>(g[i].grad);
+    out.len[q] = g[i].len;
+    out.src_type[q] = static_cast<uint8_t>(g[i].dtype);
+    out.dst_type[q] = static_cast<uint8_t>(g[i].out ? g[i].out_dtype : g[i].dtype);
+    out.first[q] = static_cast<int>(chunks);
+    chunks += (g[i].len + kGradChunk - 1) / kGradChunk;
+  }
+  out.first[out.n] = static_cast<int>(chunks);
+}
+
+long long total_chunks(const bfmoe_grad* g, int n) {
+  long long c = 0;
+  for (int i = 0; i < n; ++i) c += (g[i].len + kGradChunk - 1) / kGradChunk;
+  return c;
+}
+
+// The squares of the whole list into part; *parts: how many partial sums.
+int launch_norm(const char* what, const bfmoe_grad* g, int n, double* part, int* parts, cudaStream_t s) {
+  *parts = 0;
+  const int lists = (n + kGradsPerLaunch - 1) / kGradsPerLaunch;
+  const int cap = lists ? std::min(sm_count() * 4, kGradMaxParts / lists) : 0;
+  GradList l;
+  for (int q = 0; q < lists; ++q) {
+    fill_list(g, q * kGradsPerLaunch, std::min(n, (q + 1) * kGradsPerLaunch), l);
+    if (l.first[l.n] == 0) continue;
+    const int grid = std::min(l.first[l.n], cap);
+    const cudaError_t e = launch("grad_norm", s, [&] { grad_norm_kernel<<<grid, kGradThreads, 0, s>>>(l, part + *parts); });
+    if (e != cudaSuccess) return cuda_fail(e, what);
+    *parts += grid;
+  }
+  return BFMOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t bfmoe_route_workspace_size(int n_experts, int T, int k) {
+  if (check_routing_sizes("route_workspace_size", n_experts, T, k, n_experts, BFMOE_F32) != BFMOE_OK) return 0;
+  return make_route_plan(n_experts, T, k).total;
+}
+
+int bfmoe_route(const void* logits, int dtype, int T, long long ld, int n_experts, int k, const bfmoe_scoring* scoring,
+                const float* balance_bias, int32_t* idx, float* gates, int32_t* counts, int32_t* offsets,
+                int32_t* rows, void* ws, size_t ws_bytes, bfmoe_stream_t stream) {
+  const int N = n_experts;
+  int rc = check_routing_sizes("route", N, T, k, ld, dtype);
+  if (rc || (rc = check_scoring("route", scoring, N, k))) return rc;
+  const bool buckets = counts || offsets || rows;
+  if (buckets && (!counts || !offsets || (!rows && T > 0)))
+    return fail(BFMOE_EINVAL, "route: counts, offsets and rows must be all given or all NULL");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (T == 0) {
+    if (!buckets) return ok();
+    if ((e = cudaMemsetAsync(counts, 0, sizeof(int32_t) * N, s)) != cudaSuccess ||
+        (e = cudaMemsetAsync(offsets, 0, sizeof(int32_t) * (N + 1), s)) != cudaSuccess)
+      return cuda_fail(e, "route: memset");
+    return ok();
+  }
+  if (!logits || !idx || !gates) return fail(BFMOE_EINVAL, "route: NULL pointer");
+  if ((rc = check_elem_align("route", "logits", logits, dtype))) return rc;
+  const RoutePlan p = make_route_plan(N, T, k);
+  if (buckets && (rc = check_space("route", ws, ws_bytes, p.total))) return rc;
+  const RouteCfg cfg = cfg_of(scoring);
+  const int grid = grid_for(T, kRouteWarps, sm_count() * 8);
+  e = launch("route", s, [&] {
+    if (dtype == BFMOE_BF16)
+      route_kernel<<<grid, kRouteWarps * 32, 0, s>>>(static_cast<const __nv_bfloat16*>(logits), ld, T, N, k, cfg,
+                                                     balance_bias, idx, gates);
+    else
+      route_kernel<<<grid, kRouteWarps * 32, 0, s>>>(static_cast<const float*>(logits), ld, T, N, k, cfg,
+                                                     balance_bias, idx, gates);
+  });
+  if (e != cudaSuccess) return cuda_fail(e, "route: launch");
+  if (!buckets) return ok();
+  uint8_t* W = static_cast<uint8_t*>(ws);
+  e = build_buckets(idx, static_cast<long long>(T) * k, k, N, false, reinterpret_cast<int32_t*>(W + p.chunk_counts),
+                    reinterpret_cast<int32_t*>(W + p.totals), counts, offsets, rows, nullptr, 0, s);
+  if (e != cudaSuccess) return cuda_fail(e, "route: buckets");
+  return ok();
+}
+
+int bfmoe_balance_loss(const void* logits, int dtype, int T, long long ld, int n_experts, int k, int score,
+                       const int32_t* idx, float* loss, int32_t* load, void* ws, size_t ws_bytes,
+                       bfmoe_stream_t stream) {
+  const int N = n_experts;
+  int rc = check_routing_sizes("balance_loss", N, T, k, ld, dtype);
+  if (rc) return rc;
+  if (score != BFMOE_SCORE_SOFTMAX && score != BFMOE_SCORE_SIGMOID)
+    return fail(BFMOE_EINVAL, "balance_loss: score=%d is not softmax or sigmoid", score);
+  if (!loss || !load || (T > 0 && (!logits || !idx))) return fail(BFMOE_EINVAL, "balance_loss: NULL pointer");
+  if ((rc = check_elem_align("balance_loss", "logits", logits, dtype))) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (T == 0) {
+    if ((e = cudaMemsetAsync(load, 0, sizeof(int32_t) * (N + 1), s)) != cudaSuccess ||
+        (e = cudaMemsetAsync(loss, 0, 2 * sizeof(float), s)) != cudaSuccess)
+      return cuda_fail(e, "balance_loss: memset");
+    return ok();
+  }
+  const RoutePlan p = make_route_plan(N, T, k);
+  if ((rc = check_space("balance_loss", ws, ws_bytes, p.total))) return rc;
+  uint8_t* W = static_cast<uint8_t*>(ws);
+  float* part = reinterpret_cast<float*>(W + p.part);
+  double* zpart = reinterpret_cast<double*>(W + p.zpart);
+  if ((e = cudaMemsetAsync(load, 0, sizeof(int32_t) * (N + 1), s)) != cudaSuccess) return cuda_fail(e, "balance_loss: memset");
+  const int grid = std::min(kBalanceBlocks, grid_for(T, kGradWarps, kBalanceBlocks));
+  const size_t smem = static_cast<size_t>(kGradWarps) * N * sizeof(float);
+  static std::atomic<uint64_t> done{0};
+  if (needs_attr(done)) {
+    const int most = kGradWarps * BFMOE_MAX_EXPERTS * 4;
+    if ((e = cudaFuncSetAttribute(balance_rows_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(balance_rows_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess)
+      return cuda_fail(e, "balance_loss: attribute");
+    attr_set(done);
+  }
+  e = launch("balance_rows", s, [&] {
+    if (dtype == BFMOE_BF16)
+      balance_rows_kernel<<<grid, kGradWarps * 32, smem, s>>>(static_cast<const __nv_bfloat16*>(logits), ld, T, N, k,
+                                                              score, idx, part, zpart, load);
+    else
+      balance_rows_kernel<<<grid, kGradWarps * 32, smem, s>>>(static_cast<const float*>(logits), ld, T, N, k, score,
+                                                              idx, part, zpart, load);
+  });
+  if (e != cudaSuccess) return cuda_fail(e, "balance_loss: launch");
+  e = launch("balance_finish", s, [&] { balance_finish_kernel<<<1, 1024, 0, s>>>(part, zpart, grid, N, k, load, loss); });
+  if (e != cudaSuccess) return cuda_fail(e, "balance_loss: launch");
+  return ok();
+}
+
+int bfmoe_route_backward(const void* logits, int dtype, int T, long long ld, int n_experts, int k,
+                         const bfmoe_scoring* scoring, const int32_t* idx, const float* dgates, const int32_t* load,
+                         const float* dloss, void* dlogits, long long ld_dlogits, bfmoe_stream_t stream) {
+  const int N = n_experts;
+  int rc = check_routing_sizes("route_backward", N, T, k, ld, dtype);
+  if (rc || (rc = check_scoring("route_backward", scoring, N, k))) return rc;
+  if (ld_dlogits < N) return fail(BFMOE_EINVAL, "route_backward: row stride %lld of dlogits is less than n_experts=%d", ld_dlogits, N);
+  if ((load == nullptr) != (dloss == nullptr)) return fail(BFMOE_EINVAL, "route_backward: load and dloss must both be given or both NULL");
+  if (T == 0) return ok();
+  if (!logits || !dlogits || (dgates && !idx)) return fail(BFMOE_EINVAL, "route_backward: NULL pointer");
+  if ((rc = check_elem_align("route_backward", "logits", logits, dtype)) ||
+      (rc = check_elem_align("route_backward", "dlogits", dlogits, dtype)))
+    return rc;
+  if (logits == dlogits && ld != ld_dlogits) return fail(BFMOE_EINVAL, "route_backward: in place with another row stride");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const RouteCfg cfg = cfg_of(scoring);
+  const int grid = grid_for(T, kGradWarps, sm_count() * 8);
+  const cudaError_t e = launch("route_backward", s, [&] {
+    if (dtype == BFMOE_BF16)
+      route_backward_kernel<<<grid, kGradWarps * 32, 0, s>>>(static_cast<const __nv_bfloat16*>(logits), ld, T, N, k,
+                                                             cfg, idx, dgates, load, dloss,
+                                                             static_cast<__nv_bfloat16*>(dlogits), ld_dlogits);
+    else
+      route_backward_kernel<<<grid, kGradWarps * 32, 0, s>>>(static_cast<const float*>(logits), ld, T, N, k, cfg, idx,
+                                                             dgates, load, dloss, static_cast<float*>(dlogits),
+                                                             ld_dlogits);
+  });
+  if (e != cudaSuccess) return cuda_fail(e, "route_backward: launch");
+  return ok();
+}
+
+size_t bfmoe_grad_workspace_size(void) { return kGradMaxParts * sizeof(double); }
+
+int bfmoe_grad_norm(const bfmoe_grad* grads, int n, float* norm, void* ws, size_t ws_bytes, bfmoe_stream_t stream) {
+  int rc = check_grads("grad_norm", grads, n, false);
+  if (rc) return rc;
+  if (!norm) return fail(BFMOE_EINVAL, "grad_norm: NULL norm");
+  if (total_chunks(grads, n) > 0x7fffffffLL) return fail(BFMOE_EUNSUPPORTED, "grad_norm: too many elements");
+  if ((rc = check_space("grad_norm", ws, ws_bytes, bfmoe_grad_workspace_size()))) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  double* part = static_cast<double*>(ws);
+  int parts = 0;
+  if ((rc = launch_norm("grad_norm: launch", grads, n, part, &parts, s))) return rc;
+  const cudaError_t e = launch("grad_norm_finish", s, [&] { grad_norm_finish_kernel<<<1, kGradThreads, 0, s>>>(part, parts, norm); });
+  if (e != cudaSuccess) return cuda_fail(e, "grad_norm: launch");
+  return ok();
+}
+
+int bfmoe_grad_clip(const bfmoe_grad* grads, int n, float max_norm, float* norm, void* ws, size_t ws_bytes,
+                    bfmoe_stream_t stream) {
+  int rc = check_grads("grad_clip", grads, n, true);
+  if (rc) return rc;
+  if (!norm) return fail(BFMOE_EINVAL, "grad_clip: NULL norm");
+  if (!(max_norm >= 0.f)) return fail(BFMOE_EINVAL, "grad_clip: max_norm must be >= 0");
+  if (total_chunks(grads, n) > 0x7fffffffLL) return fail(BFMOE_EUNSUPPORTED, "grad_clip: too many elements");
+  if ((rc = check_overlap("grad_clip", grads, n))) return rc;
+  if ((rc = check_space("grad_clip", ws, ws_bytes, bfmoe_grad_workspace_size()))) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  double* part = static_cast<double*>(ws);
+  int parts = 0;
+  if ((rc = launch_norm("grad_clip: launch", grads, n, part, &parts, s))) return rc;
+  cudaError_t e;
+  GradList l;
+  float* out_norm = norm;
+  for (int i0 = 0; i0 < n; i0 += kGradsPerLaunch) {
+    fill_list(grads, i0, std::min(n, i0 + kGradsPerLaunch), l);
+    if (l.first[l.n] == 0) continue;
+    const int grid = std::min(l.first[l.n], sm_count() * 4);
+    e = launch("grad_scale", s, [&] { grad_scale_kernel<<<grid, kGradThreads, 0, s>>>(l, part, parts, max_norm, out_norm); });
+    if (e != cudaSuccess) return cuda_fail(e, "grad_clip: launch");
+    out_norm = nullptr;  // written once
+  }
+  if (out_norm) {  // nothing to scale: the norm of an empty list
+    e = launch("grad_norm_finish", s, [&] { grad_norm_finish_kernel<<<1, kGradThreads, 0, s>>>(part, parts, norm); });
+    if (e != cudaSuccess) return cuda_fail(e, "grad_clip: launch");
+  }
+  return ok();
+}
+
+}  // extern "C"
