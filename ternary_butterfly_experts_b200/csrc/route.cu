@@ -202,6 +202,35 @@ int launch_norm(const char* what, const bfmoe_grad* g, int n, double* part, int*
   return BFMOE_OK;
 }
 
+template <class S, typename Tl>
+cudaError_t launch_route_fast(const Tl* logits, long long ld, int T, int N, int k, const RouteCfg& cfg,
+                              const float* bias, int32_t* idx, float* gates, cudaStream_t s) {
+  const bool grouped = cfg.top_groups < cfg.n_groups;
+  int lpg = 1;  // lanes of a group
+  while (grouped && 2 * lpg * cfg.n_groups <= S::LPR) lpg *= 2;
+  const size_t smem = (S::MAXN + (grouped ? static_cast<size_t>(kRouteWarps) * S::ROWS * S::MAXN : 0)) * sizeof(float);
+  const int grid = grid_for(T, kRouteWarps * S::ROWS, sm_count() * 4);
+  const bool wide = wide_rows<S, Tl>(logits, ld, N);
+  return launch("route", s, [&] {
+    route_fast_kernel<S, Tl><<<grid, kRouteWarps * 32, smem, s>>>(logits, ld, T, N, k, cfg, bias, wide, lpg, idx, gates);
+  });
+}
+
+// A row's logits in the registers of 16 or 32 lanes up to 1024 experts.
+template <typename Tl>
+cudaError_t launch_route(const Tl* logits, long long ld, int T, int N, int k, const RouteCfg& cfg, const float* bias,
+                         int32_t* idx, float* gates, cudaStream_t s) {
+  if (N <= 64) return launch_route_fast<RowShape<16, 4>>(logits, ld, T, N, k, cfg, bias, idx, gates, s);
+  if (N <= 128) return launch_route_fast<RowShape<16, 8>>(logits, ld, T, N, k, cfg, bias, idx, gates, s);
+  if (N <= 256) return launch_route_fast<RowShape<32, 8>>(logits, ld, T, N, k, cfg, bias, idx, gates, s);
+  if (N <= 512) return launch_route_fast<RowShape<32, 16>>(logits, ld, T, N, k, cfg, bias, idx, gates, s);
+  if (N <= 1024) return launch_route_fast<RowShape<32, 32>>(logits, ld, T, N, k, cfg, bias, idx, gates, s);
+  return launch("route", s, [&] {
+    route_kernel<<<grid_for(T, kRouteWarps, sm_count() * 8), kRouteWarps * 32, 0, s>>>(logits, ld, T, N, k, cfg, bias,
+                                                                                       idx, gates);
+  });
+}
+
 }  // namespace
 
 extern "C" {
@@ -234,15 +263,9 @@ int bfmoe_route(const void* logits, int dtype, int T, long long ld, int n_expert
   const RoutePlan p = make_route_plan(N, T, k);
   if (buckets && (rc = check_space("route", ws, ws_bytes, p.total))) return rc;
   const RouteCfg cfg = cfg_of(scoring);
-  const int grid = grid_for(T, kRouteWarps, sm_count() * 8);
-  e = launch("route", s, [&] {
-    if (dtype == BFMOE_BF16)
-      route_kernel<<<grid, kRouteWarps * 32, 0, s>>>(static_cast<const __nv_bfloat16*>(logits), ld, T, N, k, cfg,
-                                                     balance_bias, idx, gates);
-    else
-      route_kernel<<<grid, kRouteWarps * 32, 0, s>>>(static_cast<const float*>(logits), ld, T, N, k, cfg,
-                                                     balance_bias, idx, gates);
-  });
+  e = dtype == BFMOE_BF16
+          ? launch_route(static_cast<const __nv_bfloat16*>(logits), ld, T, N, k, cfg, balance_bias, idx, gates, s)
+          : launch_route(static_cast<const float*>(logits), ld, T, N, k, cfg, balance_bias, idx, gates, s);
   if (e != cudaSuccess) return cuda_fail(e, "route: launch");
   if (!buckets) return ok();
   uint8_t* W = static_cast<uint8_t*>(ws);

@@ -16,16 +16,6 @@
 
 namespace bfmoe {
 
-// exp(l - m) with a row maximum of +inf shared among the +inf logits.
-__device__ __forceinline__ float unit_softmax(float l, float m) {
-  return m == INFINITY ? (l == INFINITY ? 1.f : 0.f) : expf(l - m);
-}
-// sigmoid(l) over exp(low), low = min(row maximum, 0)
-__device__ __forceinline__ float unit_sigmoid(float l, float low) {
-  return l > 0.f ? 1.f / (1.f + expf(-l)) : expf(l - low) / (1.f + expf(l));
-}
-__device__ __forceinline__ float sigmoid_f32(float l) { return 1.f / (1.f + expf(-l)); }
-
 constexpr int kGradWarps = 8;
 
 // Sums of one row for the losses.
@@ -178,9 +168,9 @@ __global__ __launch_bounds__(kGradWarps * 32) void route_backward_kernel(
         const float dot = warp_sum(q * dg);
         d = q * (dg - dot);
       } else {
-        d = live ? dg * sigmoid_f32(l) : 0.f;
+        d = live ? dg * sigmoid_fast(l) : 0.f;
       }
-      if (sig) d = live ? d * sigmoid_f32(-l) : 0.f;
+      if (sig) d = live ? d * sigmoid_fast(-l) : 0.f;
     }
     float fp = 0.f;
     if (load && cb != 0.f) {
@@ -204,7 +194,7 @@ __global__ __launch_bounds__(kGradWarps * 32) void route_backward_kernel(
           if (cb != 0.f) {
             const float ps = sig ? unit_sigmoid(l, low) * inv_s : p;
             float b = cb * ps * (static_cast<float>(load[q]) * fs - fp);
-            if (sig) b *= sigmoid_f32(-l);
+            if (sig) b *= sigmoid_fast(-l);
             g += b;
           }
           if (cz != 0.f) g += cz * lse * p;

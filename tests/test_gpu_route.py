@@ -154,7 +154,8 @@ def test_route_ties(N, G):
         dt = torch.bfloat16 if dtype == "bf16" else torch.float32
         zero = torch.zeros(9, N, dtype=dt)
         few = torch.randint(-2, 3, (40, N), generator=torch.Generator().manual_seed(N)).to(dt)
-        for t in (zero, few):
+        signed = torch.where(few > 0, torch.zeros_like(few), -torch.zeros_like(few))  # 0 and -0 are equal
+        for t in (zero, few, signed):
             l = t.double().numpy()
             for score in ("softmax", "sigmoid"):
                 check_route(t, l, 8, score=score)
