@@ -202,32 +202,58 @@ int launch_norm(const char* what, const bfmoe_grad* g, int n, double* part, int*
   return BFMOE_OK;
 }
 
-template <class S, typename Tl>
-cudaError_t launch_route_fast(const Tl* logits, long long ld, int T, int N, int k, const RouteCfg& cfg,
-                              const float* bias, int32_t* idx, float* gates, cudaStream_t s) {
-  const bool grouped = cfg.top_groups < cfg.n_groups;
-  int lpg = 1;  // lanes of a group
-  while (grouped && 2 * lpg * cfg.n_groups <= S::LPR) lpg *= 2;
-  const size_t smem = (S::MAXN + (grouped ? static_cast<size_t>(kRouteWarps) * S::ROWS * S::MAXN : 0)) * sizeof(float);
-  const int grid = grid_for(T, kRouteWarps * S::ROWS, sm_count() * 4);
-  const bool wide = wide_rows<S, Tl>(logits, ld, N);
+template <class S, int BY, bool GROUPED>
+cudaError_t launch_route_rows(Logits x, int T, int N, int k, const RouteCfg& cfg, const float* bias, int32_t* idx,
+                              float* gates, cudaStream_t s) {
+  int lsh = 0;  // 1 << lsh lanes take a group
+  while (GROUPED && (2 << lsh) * cfg.n_groups <= S::LPR) ++lsh;
+  x.wide = wide_rows<S>(x.p, x.ld, N, x.bf16 != 0);
+  const size_t floats = (BY != kByLogit ? S::MAXN : 0) + (GROUPED ? kRouteWarps * S::ROWS * kGroupSpace<S> : 0) +
+                        (S::V > 8 && x.wide ? kRouteWarps * 2 * S::MAXN : 0);
+  if (S::V > 8) {
+    static std::atomic<uint64_t> done{0};
+    if (needs_attr(done)) {
+      const cudaError_t e = cudaFuncSetAttribute(route_fast_kernel<S, BY, GROUPED>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (1 + kRouteWarps + 2 * kRouteWarps) * S::MAXN * 4);
+      if (e != cudaSuccess) return e;
+      attr_set(done);
+    }
+  }
+  const int grid = grid_for(T, kRouteWarps * S::ROWS, sm_count() * kRouteBlocks<S>);
   return launch("route", s, [&] {
-    route_fast_kernel<S, Tl><<<grid, kRouteWarps * 32, smem, s>>>(logits, ld, T, N, k, cfg, bias, wide, lpg, idx, gates);
+    route_fast_kernel<S, BY, GROUPED><<<grid, kRouteWarps * 32, floats * sizeof(float), s>>>(x, T, N, k, cfg, bias, lsh,
+                                                                                             idx, gates);
   });
 }
 
+template <class S>
+cudaError_t launch_route_shape(const Logits& x, int T, int N, int k, const RouteCfg& cfg, const float* bias,
+                               int32_t* idx, float* gates, cudaStream_t s) {
+  const bool grouped = cfg.top_groups < cfg.n_groups;
+  if (!bias && !(grouped && cfg.group_score == BFMOE_GROUP_TOP2)) {
+    if (grouped) return launch_route_rows<S, kByLogit, true>(x, T, N, k, cfg, bias, idx, gates, s);
+    return launch_route_rows<S, kByLogit, false>(x, T, N, k, cfg, bias, idx, gates, s);
+  }
+  if (cfg.score == BFMOE_SCORE_SOFTMAX) {
+    if (grouped) return launch_route_rows<S, kBySoftmax, true>(x, T, N, k, cfg, bias, idx, gates, s);
+    return launch_route_rows<S, kBySoftmax, false>(x, T, N, k, cfg, bias, idx, gates, s);
+  }
+  if (grouped) return launch_route_rows<S, kBySigmoid, true>(x, T, N, k, cfg, bias, idx, gates, s);
+  return launch_route_rows<S, kBySigmoid, false>(x, T, N, k, cfg, bias, idx, gates, s);
+}
+
 // A row's logits in the registers of 16 or 32 lanes up to 1024 experts.
-template <typename Tl>
-cudaError_t launch_route(const Tl* logits, long long ld, int T, int N, int k, const RouteCfg& cfg, const float* bias,
-                         int32_t* idx, float* gates, cudaStream_t s) {
-  if (N <= 64) return launch_route_fast<RowShape<16, 4>>(logits, ld, T, N, k, cfg, bias, idx, gates, s);
-  if (N <= 128) return launch_route_fast<RowShape<16, 8>>(logits, ld, T, N, k, cfg, bias, idx, gates, s);
-  if (N <= 256) return launch_route_fast<RowShape<32, 8>>(logits, ld, T, N, k, cfg, bias, idx, gates, s);
-  if (N <= 512) return launch_route_fast<RowShape<32, 16>>(logits, ld, T, N, k, cfg, bias, idx, gates, s);
-  if (N <= 1024) return launch_route_fast<RowShape<32, 32>>(logits, ld, T, N, k, cfg, bias, idx, gates, s);
+cudaError_t launch_route(const Logits& x, int T, int N, int k, const RouteCfg& cfg, const float* bias, int32_t* idx,
+                         float* gates, cudaStream_t s) {
+  if (N <= 64) return launch_route_shape<RowShape<16, 4>>(x, T, N, k, cfg, bias, idx, gates, s);
+  if (N <= 128) return launch_route_shape<RowShape<16, 8>>(x, T, N, k, cfg, bias, idx, gates, s);
+  if (N <= 256) return launch_route_shape<RowShape<32, 8>>(x, T, N, k, cfg, bias, idx, gates, s);
+  if (N <= 512) return launch_route_shape<RowShape<32, 16>>(x, T, N, k, cfg, bias, idx, gates, s);
+  if (N <= 1024) return launch_route_shape<RowShape<32, 32>>(x, T, N, k, cfg, bias, idx, gates, s);
   return launch("route", s, [&] {
-    route_kernel<<<grid_for(T, kRouteWarps, sm_count() * 8), kRouteWarps * 32, 0, s>>>(logits, ld, T, N, k, cfg, bias,
-                                                                                       idx, gates);
+    route_long_kernel<<<grid_for(T, kRouteWarps, sm_count() * 8), kRouteWarps * 32, 0, s>>>(x, T, N, k, cfg, bias, idx,
+                                                                                            gates);
   });
 }
 
@@ -263,9 +289,7 @@ int bfmoe_route(const void* logits, int dtype, int T, long long ld, int n_expert
   const RoutePlan p = make_route_plan(N, T, k);
   if (buckets && (rc = check_space("route", ws, ws_bytes, p.total))) return rc;
   const RouteCfg cfg = cfg_of(scoring);
-  e = dtype == BFMOE_BF16
-          ? launch_route(static_cast<const __nv_bfloat16*>(logits), ld, T, N, k, cfg, balance_bias, idx, gates, s)
-          : launch_route(static_cast<const float*>(logits), ld, T, N, k, cfg, balance_bias, idx, gates, s);
+  e = launch_route(Logits{logits, ld, dtype == BFMOE_BF16, 0}, T, N, k, cfg, balance_bias, idx, gates, s);
   if (e != cudaSuccess) return cuda_fail(e, "route: launch");
   if (!buckets) return ok();
   uint8_t* W = static_cast<uint8_t*>(ws);

@@ -14,6 +14,8 @@
 //           renormalised, times the scale
 // Which of two values is larger is decided as in 64 bits.
 #pragma once
+#include <algorithm>
+
 #include "common.cuh"
 
 namespace bfmoe {
@@ -53,58 +55,110 @@ __device__ __forceinline__ void warp_best(double& v, int& i) {
   }
 }
 
-// The scores of one row in 64 bits.
-struct Scores64 {
-  float M;    // the largest logit (softmax)
-  double Z;   // sum of exp(l - M)
-  int score;
-  __device__ __forceinline__ double unit(float l) const {
-    return M == INFINITY ? (l == INFINITY ? 1.0 : 0.0) : exp(static_cast<double>(l) - static_cast<double>(M));
-  }
-  __device__ __forceinline__ double of(float l) const {
-    if (score == BFMOE_SCORE_SIGMOID) return 1.0 / (1.0 + exp(-static_cast<double>(l)));
-    return unit(l) / Z;
-  }
-  // (l: not masked)
-  __device__ __forceinline__ double value(float l, const float* bias, int e) const {
-    return bias ? of(l) + static_cast<double>(bias[e]) : static_cast<double>(l);
+// exp(x) and 1 / x to about two units in the last place (plus |x| half steps
+// for the argument of exp); results below the normal range become 0.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float exp_fast(float x) { return exp2_fast(x * 1.4426950408889634f); }
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// exp(l - m), a maximum of +inf shared among the +inf logits (l not masked)
+__device__ __forceinline__ float unit_softmax(float l, float m) {
+  return m == INFINITY ? (l == INFINITY ? 1.f : 0.f) : exp_fast(l - m);
+}
+__device__ __forceinline__ float sigmoid_fast(float l) { return rcp_fast(1.f + exp_fast(-l)); }
+// sigmoid(l) over exp(low), low = min(row maximum, 0): a row of very low
+// logits keeps its ratios
+__device__ __forceinline__ float unit_sigmoid(float l, float low) {
+  return l > 0.f ? sigmoid_fast(l) : exp_fast(l - low) * rcp_fast(1.f + exp_fast(l));
+}
+
+// A matrix of logits of either type.
+struct Logits {
+  const void* p;
+  long long ld;
+  int bf16;
+  int wide;  // rows are whole cells of 16-byte aligned memory (RowShape)
+  __device__ __forceinline__ float at(int t, int e) const {
+    const long long i = static_cast<long long>(t) * ld + e;
+    return bf16 ? to_f32(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
   }
 };
 
-// Experts and gates of one row by one warp, everything in 64 bits.  Lane j
-// ends with the expert of slot j.
-template <typename Tl>
-__device__ __noinline__ void route_row_64(const Tl* row, int N, int k, const RouteCfg& cfg, const float* __restrict__ bias, int lane,
-                             int& e_out, float& gate_out) {
-  Scores64 sc;
-  sc.score = cfg.score;
-  sc.M = 0.f;
-  sc.Z = 1.0;
-  if (cfg.score == BFMOE_SCORE_SOFTMAX) {
+// The score of a logit that is not masked, in 64 bits: M and Z the row's
+// largest logit and sum of exp(l - M) (Z = 1: that term itself).  Rows that
+// need it are few and their code is not in the instruction cache: one instance
+// for all of them.
+__device__ __noinline__ double score_64(float l, float M, double Z, bool softmax) {
+  if (softmax && M == INFINITY) return (l == INFINITY ? 1.0 : 0.0) / Z;
+  const double x = exp(softmax ? static_cast<double>(l) - static_cast<double>(M) : -static_cast<double>(l));
+  return softmax ? x / Z : 1.0 / (1.0 + x);
+}
+
+// Float32 scores are off by less than this times their size (softmax: the sum
+// collects half a step a term at worst, and an exponent x of exp carries |x|
+// half steps, |x| p <= 0.37) ...
+__device__ __forceinline__ float score_eps(bool softmax, int terms) {
+  return 0x1p-23f * (softmax ? 24.f + 0.5f * static_cast<float>(terms) : 4.f);
+}
+// ... and a value by its score's error and its own rounding.
+__device__ __forceinline__ float value_eps(float eps_s, bool softmax, float score, float value) {
+  return 0x1p-23f + eps_s * (softmax ? score : 1.f) + 0x1p-23f * fabsf(value);
+}
+
+constexpr int kRouteWindow = 32;
+
+// Experts and gates of row t by one warp, decided in 64 bits: groups from
+// 64-bit values; the k best float32 values, which are the answer where values
+// are logits; else every expert whose float32 value comes within its error of
+// the k-th is ranked again by its 64-bit value (win: kRouteWindow ints of the
+// warp's shared memory; more than that many: k passes over the whole row).
+// Lane j ends with the expert of slot j.
+__device__ __noinline__ void route_row_64(const Logits& x, int t, int N, int k, const RouteCfg& cfg,
+                                          const float* __restrict__ bias, int* win, int lane, int& e_out,
+                                          float& gate_out) {
+  const bool softmax = cfg.score == BFMOE_SCORE_SOFTMAX;
+  const bool grouped = cfg.top_groups < cfg.n_groups;
+  const bool top2 = grouped && cfg.group_score == BFMOE_GROUP_TOP2;
+  float M = 0.f;
+  double Z = 1.0;
+  if (softmax && (bias || top2 || !cfg.renorm)) {
     float m = -INFINITY;
-    for (int e = lane; e < N; e += 32) m = fmaxf(m, to_f32(row[e]));  // fmaxf drops NaN
-    sc.M = warp_max(m);
+    for (int e = lane; e < N; e += 32) m = fmaxf(m, x.at(t, e));  // fmaxf drops NaN
+    M = warp_max(m);
     double z = 0.0;
+#pragma unroll 1
     for (int e = lane; e < N; e += 32) {
-      const float l = to_f32(row[e]);
-      if (!masked_logit(l)) z += sc.unit(l);
+      const float l = x.at(t, e);
+      if (!masked_logit(l)) z += score_64(l, M, 1.0, true);
     }
-    sc.Z = warp_sum(z);
+    Z = warp_sum(z);
   }
+  // -inf: masked
+  auto value64 = [&](int e, bool score) {
+    const float l = x.at(t, e);
+    double v = -INFINITY;
+    if (!masked_logit(l)) v = bias || score ? score_64(l, M, Z, softmax) : static_cast<double>(l);
+    if (bias) v += static_cast<double>(bias[e]);
+    return v > -INFINITY ? v : -INFINITY;  // NaN
+  };
   const int per = N / cfg.n_groups;
   unsigned long long kept = ~0ull;
-  if (cfg.top_groups < cfg.n_groups) {
+  if (grouped) {
     // group values: lane g % 32 holds groups g and g + 32
     double gv[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
     for (int g = 0; g < cfg.n_groups; ++g) {
       double a = -INFINITY, b = -INFINITY;  // the two best of the group
+#pragma unroll 1
       for (int q = lane; q < per; q += 32) {
-        const int e = g * per + q;
-        const float l = to_f32(row[e]);
-        if (masked_logit(l)) continue;
-        double v = sc.value(l, bias, e);
-        if (!(v > -INFINITY)) continue;
-        if (cfg.group_score == BFMOE_GROUP_TOP2 && !bias) v = sc.of(l);
+        const double v = value64(g * per + q, top2);
         if (v > a) {
           b = a;
           a = v;
@@ -118,7 +172,7 @@ __device__ __noinline__ void route_row_64(const Tl* row, int N, int k, const Rou
         b = fmax(fmin(a, oa), fmax(b, ob));
         a = fmax(a, oa);
       }
-      if (cfg.group_score == BFMOE_GROUP_TOP2 && b > -INFINITY) a += b;
+      if (top2 && b > -INFINITY) a += b;
       if ((g & 31) == lane) gv[g >> 5] = a;
     }
     kept = 0ull;
@@ -137,81 +191,119 @@ __device__ __noinline__ void route_row_64(const Tl* row, int N, int k, const Rou
       kept |= 1ull << i;
     }
   }
-  double pv = INFINITY;
-  int pi = -1;
+  auto candidate = [&](int e) { return !grouped || ((kept >> (e / per)) & 1ull); };
+  const float inv_z = softmax ? static_cast<float>(1.0 / Z) : 1.f;
+  auto score32 = [&](float l) { return softmax ? unit_softmax(l, M) * inv_z : sigmoid_fast(l); };
+  auto value32 = [&](int e) {  // -inf: masked
+    const float l = x.at(t, e);
+    if (masked_logit(l)) return -INFINITY;
+    return bias ? fmaxf(score32(l) + bias[e], -INFINITY) : l;
+  };
   int mine = 0;
+  // the k best in float32
+  float pv = INFINITY;
+  int pi = -1;
   for (int j = 0; j < k; ++j) {
-    double v = -INFINITY;
+    float v = -INFINITY;
     int i = 0x7fffffff;
     for (int e = lane; e < N; e += 32) {
-      if (!((kept >> (cfg.n_groups > 1 ? e / per : 0)) & 1ull)) continue;
-      const float l = to_f32(row[e]);
-      double c = masked_logit(l) ? -INFINITY : sc.value(l, bias, e);
-      if (!(c > -INFINITY)) c = -INFINITY;
+      if (!candidate(e)) continue;
+      const float c = value32(e);
       if (!(c < pv || (c == pv && e > pi))) continue;  // ranks before the last pick
       if (c > v || (c == v && e < i)) {
         v = c;
         i = e;
       }
     }
-    warp_best(v, i);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float ov = __shfl_xor_sync(FULL_MASK, v, o);
+      const int oi = __shfl_xor_sync(FULL_MASK, i, o);
+      if (ov > v || (ov == v && oi < i)) {
+        v = ov;
+        i = oi;
+      }
+    }
     pv = v;
     pi = i;
     if (lane == j) mine = i;
+  }
+  if (bias && pv < INFINITY) {
+    const float eps_s = score_eps(softmax, N / 32);
+    // (fewer than k experts left: everything is looked at)
+    const float near = pv > -INFINITY ? pv - 2.f * value_eps(eps_s, softmax, 1.f, pv) : -INFINITY;
+    int n = 0;
+    __syncwarp();
+    for (int e0 = 0; e0 < N; e0 += 32) {
+      const int e = e0 + lane;
+      const bool in = e < N && candidate(e) && value32(e) >= near;
+      const unsigned b = __ballot_sync(FULL_MASK, in);
+      const int at = n + __popc(b & ((1u << lane) - 1u));
+      if (in && at < kRouteWindow) win[at] = e;
+      n += __popc(b);
+    }
+    __syncwarp();
+    if (n <= kRouteWindow) {
+      double v = -INFINITY;
+      int e = 0x7fffffff;
+      if (lane < n) {
+        e = win[lane];
+        v = value64(e, false);
+      }
+      int rank = 0;
+      for (int o = 0; o < n; ++o) {
+        const double ov = __shfl_sync(FULL_MASK, v, o);
+        const int oe = __shfl_sync(FULL_MASK, e, o);
+        rank += ov > v || (ov == v && oe < e);
+      }
+      __syncwarp();
+      if (lane < n) win[rank] = e;
+      __syncwarp();
+      if (lane < k) mine = win[lane];
+      __syncwarp();
+    } else {
+      double pv64 = INFINITY;
+      pi = -1;
+      for (int j = 0; j < k; ++j) {
+        double v = -INFINITY;
+        int i = 0x7fffffff;
+        for (int e = lane; e < N; e += 32) {
+          if (!candidate(e)) continue;
+          const double c = value64(e, false);
+          if (!(c < pv64 || (c == pv64 && e > pi))) continue;
+          if (c > v || (c == v && e < i)) {
+            v = c;
+            i = e;
+          }
+        }
+        warp_best(v, i);
+        pv64 = v;
+        pi = i;
+        if (lane == j) mine = i;
+      }
+    }
   }
   // gates: lane j < k
   float l = -INFINITY;
   bool live = false;
   if (lane < k) {
-    l = to_f32(row[mine]);
-    live = !masked_logit(l) && sc.value(l, bias, mine) > -INFINITY;
+    l = x.at(t, mine);
+    live = value32(mine) > -INFINITY;
   }
-  double u = 0.0;
-  if (!cfg.renorm) {
-    u = live ? sc.of(l) : 0.0;
-  } else {
-    const float m = warp_max(live ? l : -INFINITY);
-    if (live) {
-      if (cfg.score == BFMOE_SCORE_SOFTMAX) {
-        u = m == INFINITY ? (l == INFINITY ? 1.0 : 0.0) : exp(static_cast<double>(l) - static_cast<double>(m));
-      } else {
-        // over exp(min(m, 0)), so that a row of very low logits keeps its ratios
-        const double low = m < 0.f ? static_cast<double>(m) : 0.0;
-        u = l > 0.f ? 1.0 / (1.0 + exp(-static_cast<double>(l)))
-                    : exp(static_cast<double>(l) - low) / (1.0 + exp(static_cast<double>(l)));
-      }
-    }
-    const double s = warp_sum(u);
-    u = s > 0.0 ? u / s : 0.0;
+  float u = 0.f;
+  if (cfg.renorm) {
+    const float top = warp_max(live ? l : -INFINITY);
+    if (live) u = softmax ? unit_softmax(l, top) : unit_sigmoid(l, fminf(top, 0.f));
+    const float sum = warp_sum(u);
+    u = sum > 0.f ? u / sum : 0.f;
+  } else if (live) {
+    u = score32(l);
   }
   e_out = mine;
-  gate_out = static_cast<float>(u) * cfg.scale;
+  gate_out = u * cfg.scale;
 }
 
 constexpr int kRouteWarps = 8;
-
-// exp(x) and 1 / x to about two units in the last place (plus |x| half steps
-// for the argument of exp); results below the normal range become 0.
-__device__ __forceinline__ float exp_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
-  return y;
-}
-__device__ __forceinline__ float rcp_fast(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// exp(l - m), a maximum of +inf shared among the +inf logits (l not masked)
-__device__ __forceinline__ float unit_softmax(float l, float m) {
-  return m == INFINITY ? (l == INFINITY ? 1.f : 0.f) : exp_fast(l - m);
-}
-__device__ __forceinline__ float sigmoid_fast(float l) { return rcp_fast(1.f + exp_fast(-l)); }
-// sigmoid(l) over exp(low), low = min(row maximum, 0): a row of very low
-// logits keeps its ratios
-__device__ __forceinline__ float unit_sigmoid(float l, float low) {
-  return l > 0.f ? sigmoid_fast(l) : exp_fast(l - low) * rcp_fast(1.f + exp_fast(l));
-}
 
 // Unsigned integers in the order of the floats (no NaN).
 __device__ __forceinline__ uint32_t ordered(float v) {
@@ -260,71 +352,141 @@ struct RowShape {
   static constexpr int LPR = LPR_, V = V_;
   static constexpr int CE = V < 8 ? V : 8;
   static constexpr int C = V / CE;
-  static constexpr int IB = CE == 8 ? 3 : (CE == 4 ? 2 : 1);
+  static constexpr int IB = CE == 8 ? 3 : 2;
   static constexpr int CB = C == 4 ? 2 : (C == 2 ? 1 : 0);
   static constexpr int ROWS = 32 / LPR;  // rows of a warp
   static constexpr int MAXN = LPR * V;
+  static_assert(CE >= 4 && C <= 4);
 };
 
-// Loads the lane's logits of a row: -inf for masked ones and behind the row's
-// end.  wide: rows are
-// whole cells of 16-byte (float32: 32-byte cells in two) aligned memory.
-template <class S, typename Tl>
-__device__ __forceinline__ void load_row(const Tl* row, int N, int q, bool wide, float (&l)[S::V]) {
+// A row's words as they are in memory, so that the next row can be on its way
+// while one is worked on.  Words behind the row's end are -inf of its type.
+template <class S>
+struct RawRow {
+  uint32_t w[S::V];
+  __device__ __forceinline__ void load(const Logits& x, int t, int N, int q) {
+    const long long at = static_cast<long long>(t) * x.ld;
 #pragma unroll
-  for (int c = 0; c < S::C; ++c) {
-    const int e0 = (c * S::LPR + q) * S::CE;
-    if (wide) {
-      if (e0 < N) {
-        if constexpr (sizeof(Tl) == 4) {
-          static_assert(S::CE >= 4);
-#pragma unroll
-          for (int h = 0; h < S::CE; h += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(row + e0 + h);
-            l[c * S::CE + h] = v.x;
-            l[c * S::CE + h + 1] = v.y;
-            l[c * S::CE + h + 2] = v.z;
-            l[c * S::CE + h + 3] = v.w;
+    for (int c = 0; c < S::C; ++c) {
+      const int e0 = (c * S::LPR + q) * S::CE;
+      uint32_t* v = w + c * S::CE;
+      if (x.wide) {
+        if (x.bf16) {
+          const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(x.p) + at + e0;
+          if constexpr (S::CE == 8) {
+            const uint4 u = e0 < N ? *reinterpret_cast<const uint4*>(p)
+                                   : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+            v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+          } else {
+            const uint2 u = e0 < N ? *reinterpret_cast<const uint2*>(p) : make_uint2(0xff80ff80u, 0xff80ff80u);
+            v[0] = u.x, v[1] = u.y;
           }
         } else {
-          uint32_t w[S::CE / 2];
-          if constexpr (S::CE == 8) {
-            const uint4 v = *reinterpret_cast<const uint4*>(row + e0);
-            w[0] = v.x;
-            w[1] = v.y;
-            w[2] = v.z;
-            w[3] = v.w;
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(row + e0);
-            w[0] = v.x;
-            w[1] = v.y;
-          }
+          const float* p = static_cast<const float*>(x.p) + at + e0;
 #pragma unroll
-          for (int h = 0; h < S::CE / 2; ++h) {
-            l[c * S::CE + 2 * h] = __uint_as_float(w[h] << 16);
-            l[c * S::CE + 2 * h + 1] = __uint_as_float(w[h] & 0xffff0000u);
+          for (int h = 0; h < S::CE; h += 4) {
+            const uint4 u = e0 < N ? *reinterpret_cast<const uint4*>(p + h)
+                                   : make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+            v[h] = u.x, v[h + 1] = u.y, v[h + 2] = u.z, v[h + 3] = u.w;
           }
+        }
+      } else if (x.bf16) {
+        const uint16_t* p = static_cast<const uint16_t*>(x.p) + at + e0;
+#pragma unroll
+        for (int h = 0; h < S::CE / 2; ++h) {
+          const uint32_t a = e0 + 2 * h < N ? p[2 * h] : 0xff80u, b = e0 + 2 * h + 1 < N ? p[2 * h + 1] : 0xff80u;
+          v[h] = a | b << 16;
+        }
+      } else {
+        const uint32_t* p = static_cast<const uint32_t*>(x.p) + at + e0;
+#pragma unroll
+        for (int i = 0; i < S::CE; ++i) v[i] = e0 + i < N ? p[i] : 0xff800000u;
+      }
+    }
+  }
+  // The same words from a copy of the row in shared memory.
+  __device__ __forceinline__ void load_shared(const uint8_t* row, bool bf16, int N, int q) {
+#pragma unroll
+    for (int c = 0; c < S::C; ++c) {
+      const int e0 = (c * S::LPR + q) * S::CE;
+      uint32_t* v = w + c * S::CE;
+      if (bf16) {
+        uint4 u = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+        if (e0 < N) u = *reinterpret_cast<const uint4*>(row + e0 * 2);
+        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+      } else {
+#pragma unroll
+        for (int h = 0; h < S::CE; h += 4) {
+          uint4 u = make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+          if (e0 < N) u = *reinterpret_cast<const uint4*>(row + (e0 + h) * 4);
+          v[h] = u.x, v[h + 1] = u.y, v[h + 2] = u.z, v[h + 3] = u.w;
+        }
+      }
+    }
+  }
+  // The logits, NaN as -inf; of bfloat16, whose equal values meet as keys, -0
+  // as 0.
+  __device__ __forceinline__ void unpack(bool bf16, float (&l)[S::V]) const {
+#pragma unroll
+    for (int c = 0; c < S::C; ++c) {
+      if (bf16) {
+#pragma unroll
+        for (int h = 0; h < S::CE / 2; ++h) {
+          l[c * S::CE + 2 * h] = fmaxf(__uint_as_float(w[c * S::CE + h] << 16), -INFINITY) + 0.f;
+          l[c * S::CE + 2 * h + 1] = fmaxf(__uint_as_float(w[c * S::CE + h] & 0xffff0000u), -INFINITY) + 0.f;
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < S::CE; ++i) l[c * S::CE + i] = -INFINITY;
+        for (int i = 0; i < S::CE; ++i) l[c * S::CE + i] = fmaxf(__uint_as_float(w[c * S::CE + i]), -INFINITY);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < S::CE; ++i) l[c * S::CE + i] = e0 + i < N ? to_f32(row[e0 + i]) : -INFINITY;
     }
   }
-#pragma unroll
-  for (int i = 0; i < S::V; ++i) l[i] = fmaxf(l[i], -INFINITY);  // NaN becomes -inf
-}
-// Whether load_row may take its wide form for rows ld apart.
-template <class S, typename Tl>
-__host__ __device__ __forceinline__ bool wide_rows(const void* p, long long ld, int N) {
-  return N % S::CE == 0 && ld % S::CE == 0 && (reinterpret_cast<uintptr_t>(p) & (S::CE * sizeof(Tl) - 1) & 15u) == 0;
+};
+// Whether rows can be read in cells (Logits::wide).
+template <class S>
+inline bool wide_rows(const void* p, long long ld, int N, bool bf16) {
+  const size_t bytes = std::min<size_t>(16, S::CE * (bf16 ? 2 : 4));
+  return N % S::CE == 0 && ld % S::CE == 0 && reinterpret_cast<uintptr_t>(p) % bytes == 0;
 }
 
-// Scratch of the group values: a warp's rows, the values of one row.
-__host__ __device__ constexpr size_t route_group_floats(int maxn) { return static_cast<size_t>(maxn); }
+// Rows of more than 256 experts come through shared memory: one bulk copy a
+// row, a row of each warp on its way while one is worked on.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// exp(l - m) of a row and its sum over the row; masked logits give 0.
+template <class S>
+__device__ __forceinline__ float row_softmax(const float (&l)[S::V], float m, float (&u)[S::V]) {
+  if (fabsf(m) < 0x1p120f) {
+    const float ml = m * 1.4426950408889634f;
+#pragma unroll
+    for (int i = 0; i < S::V; ++i) u[i] = exp2_fast(fmaf(l[i], 1.4426950408889634f, -ml));
+  } else {  // +-inf, or masks of the type's lowest value alone
+#pragma unroll
+    for (int i = 0; i < S::V; ++i) u[i] = masked_logit(l[i]) ? 0.f : unit_softmax(l[i], m);
+  }
+  float z = 0.f;
+#pragma unroll
+  for (int i = 0; i < S::V; ++i) z += u[i];
+  return seg_sum<S::LPR>(z);
+}
+
+// What ranks the experts: the logits, or softmax or sigmoid scores (with a
+// bias, or summed up by group).
+enum { kByLogit = 0, kBySoftmax = 1, kBySigmoid = 2 };
+
+// Blocks of an SM: what the registers of a row leave room for.
+template <class S>
+constexpr int kRouteBlocks = S::V <= 8 ? 4 : (S::V <= 16 ? 3 : 2);
+
+// Floats of shared memory for the group values of a row: all values in 64 bits
+// where there is room for them.
+template <class S>
+constexpr int kGroupSpace = S::V <= 8 ? 2 * S::MAXN : S::MAXN;
 
 // A row in the registers of LPR lanes, N <= LPR * V.
 //
@@ -338,103 +500,157 @@ __host__ __device__ constexpr size_t route_group_floats(int maxn) { return stati
 // picked one, and no key has to be moved.
 // The truncated keys and the float32 scores rank two values rightly when they
 // are further apart than both errors; k + 1 picks are taken and every gap is
-// looked at.  The few rows (about 1 in 1000) with a smaller gap are settled in
-// 64 bits by the whole warp (route_row_64).
-// Values that the keys hold exactly (no bias: bfloat16 logits) need no gap.
-template <class S, typename Tl>
-__global__ __launch_bounds__(kRouteWarps * 32) void route_fast_kernel(const Tl* __restrict__ logits, long long ld,
-                                                                      int T, int N, int k, RouteCfg cfg,
-                                                                      const float* __restrict__ bias, bool wide,
-                                                                      int lpg, int32_t* __restrict__ idx,
-                                                                      float* __restrict__ gates) {
+// looked at.  A row with a smaller gap (about 1 in 1000) takes more picks until
+// a clear gap closes the list, whose experts are then ranked by their 64-bit
+// values.  Longer lists than a row's lanes are left to the whole warp
+// (route_row_64).
+// Values that the keys hold exactly (bfloat16 logits) need no gap.
+template <class S, int BY, bool GROUPED>
+__global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_kernel(
+    const Logits x, int T, int N, int k, const RouteCfg cfg, const float* __restrict__ bias, int lsh,
+    int32_t* __restrict__ idx, float* __restrict__ gates) {
   constexpr int LPR = S::LPR, V = S::V, CE = S::CE, C = S::C;
   constexpr int B = S::IB + S::CB;
   constexpr uint32_t LOW = (1u << B) - 1u;
-  extern __shared__ float route_smem[];  // bias [MAXN], then the group values
+  constexpr uint32_t MASKED = 0x007fffffu & ~LOW;  // ordered(-inf): above 0, below every value
+  constexpr bool SCORED = BY != kByLogit;
+  extern __shared__ __align__(128) float route_smem[];  // bias [MAXN] (scored), group values (grouped), rows
+  __shared__ int win_s[kRouteWarps][kRouteWindow];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int q = lane & (LPR - 1);
-  const bool softmax = cfg.score == BFMOE_SCORE_SOFTMAX;
-  const bool grouped = cfg.top_groups < cfg.n_groups;
-  const bool top2 = grouped && cfg.group_score == BFMOE_GROUP_TOP2;
-  const bool scored = bias || top2;
-  const bool need_z = softmax && (scored || !cfg.renorm);
-  const int per = N / cfg.n_groups;
+  const bool softmax = BY == kBySoftmax || (BY == kByLogit && cfg.score == BFMOE_SCORE_SOFTMAX);
+  const int per = GROUPED ? N / cfg.n_groups : N;
   const bool cells = per % CE == 0;  // no cell lies in two groups
-  float* gs = route_smem + S::MAXN + (w * S::ROWS + lane / LPR) * S::MAXN;
-  if (bias) {
-    for (int e = threadIdx.x; e < S::MAXN; e += blockDim.x) route_smem[e] = e < N ? bias[e] : 0.f;
+  float* gs = route_smem + (SCORED ? S::MAXN : 0) + (w * S::ROWS + lane / LPR) * kGroupSpace<S>;
+  if constexpr (SCORED) {
+    for (int e = threadIdx.x; e < S::MAXN; e += blockDim.x)
+      route_smem[e] = bias && e < N ? fmaxf(bias[e], -INFINITY) : 0.f;  // NaN masks
     __syncthreads();
   }
-  // float32 scores are off by less than this (times their size: the sum of a
-  // softmax collects a half step a term at worst)
-  const float eps_s = 0x1p-23f * (softmax ? 24.f + 0.5f * V : 4.f);
-  const bool exact_keys = !bias && sizeof(Tl) == 2;
+  const float eps_s = score_eps(softmax, V);
+  const bool exact_keys = x.bf16 && !bias;
+  // groups: 1 << lsh lanes take one; lane q works on group gq (+ LPR, ...),
+  // its cells begin in groups g0
+  const int lpg = 1 << lsh, gq = q >> lsh;
+  int g0[C];
+  if constexpr (GROUPED) {
+#pragma unroll
+    for (int cc = 0; cc < C; ++cc) g0[cc] = (cc * LPR + q) * CE / per;
+  }
+  const int items = cells ? per / CE : per;  // of a group
 
-  const int warps = gridDim.x * kRouteWarps;
-  for (int t0 = (blockIdx.x * kRouteWarps + w) * S::ROWS; t0 < T; t0 += warps * S::ROWS) {
-    const int t = t0 + lane / LPR;
-    const bool has = t < T;
-    const Tl* row = logits + static_cast<long long>(has ? t : t0) * ld;
-    float l[V], c[V];
-    load_row<S>(row, N, q, wide, l);
-    float m = 0.f, inv_z = 1.f;
-    if (need_z) {
-      float x = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < V; ++i) x = fmaxf(x, l[i]);
-      m = seg_max<LPR>(x);
-      float z = 0.f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        c[i] = masked_logit(l[i]) ? 0.f : unit_softmax(l[i], m);
-        z += c[i];
-      }
-      z = seg_sum<LPR>(z);
-      inv_z = z > 0.f ? 1.f / z : 0.f;
+  const int step = gridDim.x * kRouteWarps * S::ROWS;
+  int t0 = (blockIdx.x * kRouteWarps + w) * S::ROWS;
+  // Loads run ahead: rows of up to 256 experts as registers, longer ones (in
+  // cells) through two buffers of the warp in shared memory.
+  constexpr bool AHEAD = V <= 8;
+  __shared__ uint64_t full_s[AHEAD ? 1 : kRouteWarps * 2];
+  const bool staged = !AHEAD && x.wide;
+  const uint32_t row_bytes = static_cast<uint32_t>(N) * (x.bf16 ? 2u : 4u);
+  uint8_t* buf = reinterpret_cast<uint8_t*>(route_smem + (SCORED ? S::MAXN : 0) +
+                                            (GROUPED ? kRouteWarps * S::ROWS * kGroupSpace<S> : 0)) +
+                 static_cast<size_t>(w) * 2 * S::MAXN * 4;
+  uint64_t* full = full_s + w * 2;
+  auto fetch = [&](int tn, int b) {  // lane 0: row tn into buffer b
+    mbar_expect_tx(full + b, row_bytes);
+    bulk_load(buf + b * S::MAXN * 4,
+              static_cast<const uint8_t*>(x.p) + static_cast<long long>(tn) * x.ld * (x.bf16 ? 2 : 4), row_bytes, full + b);
+  };
+  int turn = 0;  // rows this warp has taken
+  if (staged) {
+    if (lane == 0) {
+      mbar_init(full, 1);
+      mbar_init(full + 1, 1);
+      mbar_fence_init();
+      if (t0 < T) fetch(t0, 0);
     }
-    if (scored) {
+    __syncwarp();
+  }
+  RawRow<S> raw;
+  if (AHEAD && t0 < T) raw.load(x, min(t0 + lane / LPR, T - 1), N, q);
+  for (; t0 < T; t0 += step) {
+    const int t = min(t0 + lane / LPR, T - 1);
+    const bool has = t0 + lane / LPR < T;
+    float l[V], c[V];
+    const uint8_t* here = nullptr;  // the row in shared memory
+    if constexpr (!AHEAD) {
+      if (staged) {
+        const int b = turn & 1;
+        // the buffer of the row before was read before that row's picks
+        if (lane == 0 && t0 + step < T) fetch(t0 + step, b ^ 1);
+        // a copy that does not come is reported; every lane sees the same
+        if (__any_sync(FULL_MASK, !mbar_wait(full + b, (turn >> 1) & 1, 0x2100u))) {
+          if (t0 + step < T) mbar_wait(full + (b ^ 1), ((turn + 1) >> 1) & 1, 0x2101u);
+          return;
+        }
+        here = buf + b * S::MAXN * 4;
+        raw.load_shared(here, x.bf16, N, q);
+        __syncwarp();
+        ++turn;
+      } else {
+        raw.load(x, t, N, q);
+      }
+    }
+    raw.unpack(x.bf16, l);
+    if (AHEAD && t0 + step < T) raw.load(x, min(t0 + step + lane / LPR, T - 1), N, q);
+    float m = 0.f, inv_z = 1.f;
+    if constexpr (BY == kBySoftmax) {
+      float h = l[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) h = fmaxf(h, l[i]);
+      m = seg_max<LPR>(h);
+      const float z = row_softmax<S>(l, m, c);
+      inv_z = z > 0.f ? rcp_fast(z) : 0.f;
+    }
+    if constexpr (SCORED) {
 #pragma unroll
       for (int cc = 0; cc < C; ++cc) {
         const int e0 = (cc * LPR + q) * CE;
-        float b[CE];
 #pragma unroll
         for (int h = 0; h < CE; h += 4) {
-          const float4 v = bias ? *reinterpret_cast<const float4*>(route_smem + e0 + h) : make_float4(0.f, 0.f, 0.f, 0.f);
-          b[h] = v.x;
-          b[h + 1] = v.y;
-          b[h + 2] = v.z;
-          b[h + 3] = v.w;
-        }
+          const float4 b = *reinterpret_cast<const float4*>(route_smem + e0 + h);
+          const float bb[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int i = 0; i < CE; ++i) {
-          const int v = cc * CE + i;
-          const float x = (softmax ? c[v] * inv_z : sigmoid_fast(l[v])) + b[i];
-          c[v] = masked_logit(l[v]) ? -INFINITY : fmaxf(x, -INFINITY);
+          for (int i = 0; i < 4; ++i) {
+            const int v = cc * CE + h + i;
+            const float s = BY == kBySoftmax ? fmaf(c[v], inv_z, bb[i]) : sigmoid_fast(l[v]) + bb[i];
+            c[v] = masked_logit(l[v]) ? -INFINITY : s;
+          }
         }
       }
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) c[i] = l[i];
     }
+    // the sum of the row's exp(l - m) in 64 bits
+    auto row_z64 = [&]() {
+      double z = 0.0;
+#pragma unroll 1
+      for (int e = q; e < N; e += LPR) {
+        const float v = x.at(t, e);
+        if (!masked_logit(v)) z += score_64(v, m, 1.0, true);
+      }
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) z += __shfl_xor_sync(FULL_MASK, z, o);
+      return z;
+    };
     // groups: the two best of each cell (or every value) go to shared memory,
     // lpg lanes take a group
     bool clear = true;
-    unsigned long long kept = ~0ull;
-    if (grouped) {
-      const int items = cells ? per / CE : per;  // of a group
+    unsigned long long kept = ~0ull;  // bit g << lsh
+    if constexpr (GROUPED) {
+      const bool top2 = cfg.group_score == BFMOE_GROUP_TOP2;
       if (cells) {
 #pragma unroll
         for (int cc = 0; cc < C; ++cc) {
           float a = -INFINITY, b = -INFINITY;
 #pragma unroll
           for (int i = 0; i < CE; ++i) {
-            const float x = c[cc * CE + i];
-            b = fmaxf(b, fminf(a, x));
-            a = fmaxf(a, x);
+            const float v = c[cc * CE + i];
+            b = fmaxf(b, fminf(a, v));
+            a = fmaxf(a, v);
           }
-          const int cell = cc * LPR + q;
-          gs[2 * cell] = a;
-          gs[2 * cell + 1] = b;
+          *reinterpret_cast<float2*>(gs + 2 * (cc * LPR + q)) = make_float2(a, b);
         }
       } else {
 #pragma unroll
@@ -444,108 +660,196 @@ __global__ __launch_bounds__(kRouteWarps * 32) void route_fast_kernel(const Tl* 
       }
       __syncwarp();
       constexpr int GH = BFMOE_MAX_GROUPS / LPR;  // groups of a lane, at most
+      const int hs = lsh == 0 ? (cfg.n_groups + LPR - 1) / LPR : 1;
       float gv[GH];
-#pragma unroll
-      for (int h = 0; h < GH; ++h) {
-        const int g = q / lpg + h * LPR;
-        float a = -INFINITY, b = -INFINITY;
-        if (g < cfg.n_groups && (h == 0 || lpg == 1)) {
-          for (int it = q % lpg; it < items; it += lpg) {
-            float oa, ob = -INFINITY;
-            if (cells) {
-              oa = gs[2 * (g * items + it)];
-              ob = gs[2 * (g * items + it) + 1];
-            } else {
-              oa = gs[g * items + it];
-            }
-            b = fmaxf(fminf(a, oa), fmaxf(b, ob));
-            a = fmaxf(a, oa);
-          }
-        }
-        if (h == 0)
-          for (int o = 1; o < lpg; o <<= 1) {
-            const float oa = __shfl_xor_sync(FULL_MASK, a, o), ob = __shfl_xor_sync(FULL_MASK, b, o);
-            b = fmaxf(fminf(a, oa), fmaxf(b, ob));
-            a = fmaxf(a, oa);
-          }
-        gv[h] = top2 && b > -INFINITY ? a + b : a;
-      }
       int rank[GH];
 #pragma unroll
-      for (int h = 0; h < GH; ++h) rank[h] = 0;
+      for (int h = 0; h < GH; ++h) {
+        gv[h] = -INFINITY;
+        rank[h] = 0;
+        if (h >= hs) continue;
+        const int g = gq + h * LPR;
+        float a = -INFINITY, b = -INFINITY;
+        if (g < cfg.n_groups) {
+          for (int it = q & (lpg - 1); it < items; it += lpg) {
+            float2 o = make_float2(-INFINITY, -INFINITY);
+            if (cells) o = *reinterpret_cast<const float2*>(gs + 2 * (g * items + it));
+            else o.x = gs[g * items + it];
+            b = fmaxf(fminf(a, o.x), fmaxf(b, o.y));
+            a = fmaxf(a, o.x);
+          }
+        }
+        for (int o = 1; o < lpg; o <<= 1) {
+          const float oa = __shfl_xor_sync(FULL_MASK, a, o), ob = __shfl_xor_sync(FULL_MASK, b, o);
+          b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+          a = fmaxf(a, oa);
+        }
+        gv[h] = top2 && b > -INFINITY ? a + b : a;
+      }
 #pragma unroll
       for (int h = 0; h < GH; ++h) {
-        const int n = min(cfg.n_groups - h * LPR, LPR / lpg);
-        for (int o = 0; o < n; ++o) {
-          const float v = __shfl_sync(FULL_MASK, gv[h], (lane & ~(LPR - 1)) + o * lpg);
-          const int g2 = o + h * LPR;
+        if (h >= hs) continue;
+        // the lanes of a group share the comparisons
+        const int n = min(cfg.n_groups - h * LPR, LPR >> lsh);
+        for (int o0 = 0; o0 < n; o0 += lpg) {
+          const int o = o0 + (q & (lpg - 1));
+          const float v = __shfl_sync(FULL_MASK, gv[h], min(o, n - 1) << lsh, LPR);
 #pragma unroll
-          for (int u = 0; u < GH; ++u) rank[u] += v > gv[u] || (v == gv[u] && g2 < q / lpg + u * LPR);
+          for (int u = 0; u < GH; ++u)
+            rank[u] += o < n && (v > gv[u] || (v == gv[u] && o + h * LPR < gq + u * LPR));
         }
       }
+      for (int o = 1; o < lpg; o <<= 1) rank[0] += __shfl_xor_sync(FULL_MASK, rank[0], o);
       float worst = INFINITY, best = -INFINITY;  // of the kept, of the others
       kept = 0ull;
 #pragma unroll
       for (int h = 0; h < GH; ++h) {
-        const int g = q / lpg + h * LPR;
-        const bool real = g < cfg.n_groups && (h == 0 || lpg == 1) && q % lpg == 0;
+        if (h >= hs) continue;
+        const bool real = gq + h * LPR < cfg.n_groups && (q & (lpg - 1)) == 0;
         const bool in = real && rank[h] < cfg.top_groups;
         if (in) worst = fminf(worst, gv[h]);
         else if (real) best = fmaxf(best, gv[h]);
-        // bit g * lpg of the ballot; moved to bit g below by the reader
         kept |= static_cast<unsigned long long>(seg_bits<LPR>(in, lane)) << (h * LPR);
       }
-      if (scored) {
+      if constexpr (SCORED) {
         worst = -seg_max<LPR>(-worst);
         best = seg_max<LPR>(best);
-        // (a sum of two scores; the score itself is at most 1)
-        const float e = 4.f * (eps_s + 0x1p-23f * (1.f + fabsf(worst)));
-        clear = !(best > -INFINITY) || worst - best > e;
-      }
-      if (scored && !bias) {
+        // (a sum of two values; a score is at most 1)
+        clear = !(best > -INFINITY) || worst - best > 4.f * value_eps(eps_s, softmax, 1.f, worst);
+        // the same in 64 bits for rows whose groups are too near each other
+        // (about 1 in 10^4), where the cells' values fit
+        if ((cells || kGroupSpace<S> >= 2 * S::MAXN) && __any_sync(FULL_MASK, !clear)) {
+          const double z64 = softmax ? row_z64() : 1.0;
+          double* gd = reinterpret_cast<double*>(gs);
+          __syncwarp();
+#pragma unroll 1
+          for (int cc = 0; cc < C; ++cc) {
+            double a = -INFINITY, b = -INFINITY;
+#pragma unroll 1
+            for (int i = 0; i < CE; ++i) {
+              const int e = (cc * LPR + q) * CE + i;
+              double v = -INFINITY;
+              if (e < N) {
+                const float le = x.at(t, e);
+                if (!masked_logit(le)) v = score_64(le, m, z64, softmax) + static_cast<double>(route_smem[e]);
+                if (!cells) gd[e] = v;
+              }
+              b = fmax(b, fmin(a, v));
+              a = fmax(a, v);
+            }
+            if (cells) {
+              gd[2 * (cc * LPR + q)] = a;
+              gd[2 * (cc * LPR + q) + 1] = b;
+            }
+          }
+          __syncwarp();
+          // lane q: groups q, q + LPR, ...
+          double gv64[GH];
+          int r64[GH];
 #pragma unroll
-        for (int i = 0; i < V; ++i) c[i] = l[i];
+          for (int h = 0; h < GH; ++h) {
+            double a = -INFINITY, b = -INFINITY;
+            const int g = q + h * LPR;
+#pragma unroll 1
+            for (int it = 0; g < cfg.n_groups && it < items; ++it) {
+              const double oa = cells ? gd[2 * (g * items + it)] : gd[g * items + it];
+              const double ob = cells ? gd[2 * (g * items + it) + 1] : -INFINITY;
+              b = fmax(fmin(a, oa), fmax(b, ob));
+              a = fmax(a, oa);
+            }
+            gv64[h] = top2 && b > -INFINITY ? a + b : a;
+            r64[h] = 0;
+          }
+#pragma unroll
+          for (int h = 0; h < GH; ++h)
+#pragma unroll 1
+            for (int o = 0; o < min(cfg.n_groups - h * LPR, LPR); ++o) {
+              const double v = __shfl_sync(FULL_MASK, gv64[h], o, LPR);
+#pragma unroll
+              for (int u = 0; u < GH; ++u)
+                r64[u] += v > gv64[u] || (v == gv64[u] && o + h * LPR < q + u * LPR);
+            }
+          unsigned long long kept64 = 0ull;  // bit g
+#pragma unroll
+          for (int h = 0; h < GH; ++h)
+            kept64 |= static_cast<unsigned long long>(
+                          seg_bits<LPR>(q + h * LPR < cfg.n_groups && r64[h] < cfg.top_groups, lane))
+                      << (h * LPR);
+          if (!clear) {
+            kept = kept64;
+            if (lsh) {
+              kept = 0ull;
+              for (int g = 0; g < cfg.n_groups; ++g) kept |= ((kept64 >> g) & 1ull) << (g << lsh);
+            }
+          }
+          clear = true;
+        }
+        if (!bias) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) c[i] = l[i];
+        }
       }
     }
-    // keys: 0 what is no candidate, then masked experts, then values
-    uint32_t key[V];
+    // keys: 0 for what is no candidate
+    uint32_t key[V], head[C];
 #pragma unroll
     for (int cc = 0; cc < C; ++cc) {
-      const int e0 = (cc * LPR + q) * CE;
-      int g = 0, r = 0;
-      bool in = true;
-      if (grouped) {
-        g = e0 / per;
-        r = e0 - g * per;
-        in = (kept >> (g * lpg)) & 1ull;
-      }
 #pragma unroll
       for (int i = 0; i < CE; ++i) {
         const uint32_t low = static_cast<uint32_t>((C - 1 - cc) * CE + (CE - 1 - i));
-        const float x = c[cc * CE + i];
-        const uint32_t o = x > -INFINITY ? (ordered(x + 0.f) & ~LOW) | low : (1u << B) | low;  // + 0: one zero
-        if (grouped && !cells) {
-          if (r == per) {
-            r = 0;
-            ++g;
-            in = (kept >> (g * lpg)) & 1ull;
-          }
-          ++r;
-        }
-        key[cc * CE + i] = in && e0 + i < N ? o : 0u;
+        key[cc * CE + i] = (ordered(c[cc * CE + i]) & ~LOW) | low;
       }
-    }
-    uint32_t head[C];
+      const int e0 = (cc * LPR + q) * CE;
+      if (N < S::MAXN) {
 #pragma unroll
-    for (int cc = 0; cc < C; ++cc) {
+        for (int i = 0; i < CE; ++i)
+          if (e0 + i >= N) key[cc * CE + i] = 0u;
+      }
+      if constexpr (GROUPED) {
+        bool in = e0 < N && ((kept >> (g0[cc] << lsh)) & 1ull);
+        if (cells) {
+#pragma unroll
+          for (int i = 0; i < CE; ++i) key[cc * CE + i] = in ? key[cc * CE + i] : 0u;
+        } else {
+          int g = g0[cc], r = e0 - g * per;
+#pragma unroll
+          for (int i = 0; i < CE; ++i) {
+            if (r == per) {
+              r = 0;
+              ++g;
+              in = e0 + i < N && ((kept >> (g << lsh)) & 1ull);
+            }
+            ++r;
+            key[cc * CE + i] = in ? key[cc * CE + i] : 0u;
+          }
+        }
+      }
       head[cc] = key[cc * CE];
 #pragma unroll
       for (int i = 1; i < CE; ++i) head[cc] = max(head[cc], key[cc * CE + i]);
     }
+    if constexpr (BY == kByLogit) {
+      if (softmax && !cfg.renorm) {
+        // any value near the largest serves as the maximum: a truncated key's
+        // (off by |m| 2^(B - 23)), unless it is large or not the row's (groups)
+        uint32_t top = head[0];
+#pragma unroll
+        for (int cc = 1; cc < C; ++cc) top = max(top, head[cc]);
+        m = from_ordered(seg_max_u32<LPR>(top) & ~LOW);
+        if (GROUPED || __any_sync(FULL_MASK, !(fabsf(m) < 1024.f))) {
+          float h = l[0];
+#pragma unroll
+          for (int i = 1; i < V; ++i) h = fmaxf(h, l[i]);
+          m = seg_max<LPR>(h);
+        }
+        const float z = row_softmax<S>(l, m, c);
+        inv_z = z > 0.f ? rcp_fast(z) : 0.f;
+      }
+    }
     // picks: lane j of the row keeps the j-th (key and lane)
     uint32_t pick = 0;
     int from = 0;
-    for (int j = 0; j <= k; ++j) {
+    auto pick_next = [&](int j) {
       uint32_t top = head[0];
 #pragma unroll
       for (int cc = 1; cc < C; ++cc) top = max(top, head[cc]);
@@ -557,38 +861,95 @@ __global__ __launch_bounds__(kRouteWarps * 32) void route_fast_kernel(const Tl* 
         pick = got;
         from = src;
       }
-      if (q == src) {
+      if (q == src && got != 0u) {
         const int cc = C - 1 - static_cast<int>((got & LOW) >> S::IB);
 #pragma unroll
         for (int u = 0; u < C; ++u)
-          if (u == cc) {
+          if (C == 1 || u == cc) {
             uint32_t d = 0u - got;
 #pragma unroll
-            for (int i = 0; i < CE; ++i) d = max(d, key[u * CE + i] - got);
+            for (int i = 0; i < CE; ++i) d = __viaddmax_u32(key[u * CE + i], 0u - got, d);
             head[u] = got + d;
           }
       }
-    }
-    // the picks' values again, the gaps between them, the gates
-    const bool valid = pick != 0u && q <= k;
-    const int place = static_cast<int>(LOW) - static_cast<int>(pick & LOW);  // c * CE + i
-    const int e = ((place / CE) * LPR + from) * CE + place % CE;
-    const bool live = valid && (pick >> B) > 1u;
+    };
+#pragma unroll 1
+    for (int j = 0; j <= k; ++j) pick_next(j);
+    // the picks' values again, the gaps between them
+    int e = 0;
+    bool live = false;
     float le = -INFINITY, sc = 0.f, val = 0.f, eps = 0.f;
-    if (live) {
-      le = to_f32(row[e]);
-      if (scored || !cfg.renorm) sc = softmax ? unit_softmax(le, m) * inv_z : sigmoid_fast(le);
-      val = bias ? sc + route_smem[e] : le;
-      if (bias) eps = 0x1p-23f + eps_s * (softmax ? sc : 1.f) + 0x1p-23f * fabsf(val);
-      if (!exact_keys) eps += fabsf(val) * (0x1p-23f * (1u << B)) + 0x1p-126f;
-    }
+    auto look_up = [&](int n) {  // lanes q < n
+      const int place = static_cast<int>(LOW) - static_cast<int>(pick & LOW);  // c * CE + i
+      e = ((place / CE) * LPR + from) * CE + place % CE;
+      live = q < n && (pick & ~LOW) > MASKED;
+      if (live) {
+        if (!AHEAD && here)
+          le = x.bf16 ? to_f32(reinterpret_cast<const __nv_bfloat16*>(here)[e]) : reinterpret_cast<const float*>(here)[e];
+        else
+          le = x.at(t, e);
+        if (bias || !cfg.renorm) sc = softmax ? unit_softmax(le, m) * inv_z : sigmoid_fast(le);
+        val = le;
+        eps = 0.f;
+        if constexpr (SCORED) {
+          if (bias) {
+            val = sc + route_smem[e];
+            eps = value_eps(eps_s, softmax, sc, val);
+          }
+        }
+        eps += fabsf(val) * (0x1p-23f * (1u << B)) + 0x1p-126f;
+      }
+    };
+    look_up(k + 1);
     if (!exact_keys) {
-      const float v2 = __shfl_down_sync(FULL_MASK, val, 1, LPR);
-      const float e2 = __shfl_down_sync(FULL_MASK, eps, 1, LPR);
-      const bool l2 = __shfl_down_sync(FULL_MASK, live ? 1 : 0, 1, LPR) != 0;
-      const bool near = q < k && l2 && !(val - v2 > eps + e2);
-      const unsigned nears = seg_bits<LPR>(near, lane);  // by every lane, whatever its row's groups said
-      clear = clear && nears == 0u;
+      auto gaps = [&]() {  // bit q: picks q and q + 1 are too near each other
+        const float v2 = __shfl_down_sync(FULL_MASK, val, 1, LPR);
+        const float e2 = __shfl_down_sync(FULL_MASK, eps, 1, LPR);
+        const bool l2 = __shfl_down_sync(FULL_MASK, live ? 1 : 0, 1, LPR) != 0;
+        return seg_bits<LPR>(q + 1 < LPR && l2 && !(val - v2 > eps + e2), lane);
+      };
+      unsigned near = gaps();
+      if (__any_sync(FULL_MASK, near != 0u)) {
+        // more picks, until a gap behind the k-th closes the list
+        int n = k + 1;
+        unsigned ends = (~near >> (k - 1)) & ((1u << (n - k)) - 1u);
+        while (n < LPR && __any_sync(FULL_MASK, near != 0u && ends == 0u)) {
+          pick_next(n);
+          look_up(++n);
+          near = gaps();
+          ends = (~near >> (k - 1)) & ((1u << (n - k)) - 1u);
+        }
+        // the list's experts in the order of their 64-bit values
+        const bool settle = near != 0u && ends != 0u;
+        clear = clear && (near == 0u || ends != 0u);
+        const int len = k - 1 + __ffs(ends);
+        const double z64 = BY == kBySoftmax && bias ? row_z64() : 1.0;
+        double v64 = -INFINITY;
+        if (live) {
+          v64 = static_cast<double>(le);
+          if (SCORED && bias) v64 = score_64(le, m, z64, softmax) + static_cast<double>(route_smem[e]);
+        }
+        int rank = 0;
+        for (int o = 0; o < n; ++o) {
+          const double ov = __shfl_sync(FULL_MASK, v64, o, LPR);
+          const int oe = __shfl_sync(FULL_MASK, e, o, LPR);
+          rank += o < len && (ov > v64 || (ov == v64 && oe < e));
+        }
+        const int e_old = e;
+        const float l_old = le, s_old = sc;
+        const int live_old = live ? 1 : 0;
+        for (int o = 0; o < n; ++o) {
+          const int r = __shfl_sync(FULL_MASK, rank, o, LPR), oe = __shfl_sync(FULL_MASK, e_old, o, LPR);
+          const float ol = __shfl_sync(FULL_MASK, l_old, o, LPR), os = __shfl_sync(FULL_MASK, s_old, o, LPR);
+          const int ov = __shfl_sync(FULL_MASK, live_old, o, LPR);
+          if (settle && o < len && r == q) {
+            e = oe;
+            le = ol;
+            sc = os;
+            live = ov != 0;
+          }
+        }
+      }
     }
     const bool mine = q < k && live;
     float u = 0.f;
@@ -596,7 +957,7 @@ __global__ __launch_bounds__(kRouteWarps * 32) void route_fast_kernel(const Tl* 
       const float top = seg_max<LPR>(mine ? le : -INFINITY);
       if (mine) u = softmax ? unit_softmax(le, top) : unit_sigmoid(le, fminf(top, 0.f));
       const float sum = seg_sum<LPR>(u);
-      u = sum > 0.f ? u / sum : 0.f;
+      u = sum > 0.f ? u * rcp_fast(sum) : 0.f;
     } else if (mine) {
       u = sc;
     }
@@ -610,28 +971,29 @@ __global__ __launch_bounds__(kRouteWarps * 32) void route_fast_kernel(const Tl* 
       open &= open - 1;
       int e2;
       float g2;
-      route_row_64(logits + static_cast<long long>(t2) * ld, N, k, cfg, bias, lane, e2, g2);
+      route_row_64(x, t2, N, k, cfg, bias, win_s[w], lane, e2, g2);
       if (lane < k) {
         idx[static_cast<long long>(t2) * k + lane] = e2;
         gates[static_cast<long long>(t2) * k + lane] = g2;
       }
     }
-    if (grouped) __syncwarp();  // the group values are read before the next row's are written
+    if (GROUPED) __syncwarp();  // the group values are read before the next row's are written
   }
 }
 
-template <typename Tl>
-__global__ __launch_bounds__(kRouteWarps * 32) void route_kernel(const Tl* __restrict__ logits, long long ld, int T,
-                                                                 int N, int k, RouteCfg cfg,
-                                                                 const float* __restrict__ bias,
-                                                                 int32_t* __restrict__ idx,
-                                                                 float* __restrict__ gates) {
-  const int lane = threadIdx.x & 31;
-  const int warps = gridDim.x * kRouteWarps;
-  for (int t = blockIdx.x * kRouteWarps + (threadIdx.x >> 5); t < T; t += warps) {
+// Rows of more experts than registers hold: a warp a row, several passes over
+// it (it stays in the caches).
+__global__ __launch_bounds__(kRouteWarps * 32) void route_long_kernel(const Logits x, int T, int N, int k,
+                                                                      const RouteCfg cfg,
+                                                                      const float* __restrict__ bias,
+                                                                      int32_t* __restrict__ idx,
+                                                                      float* __restrict__ gates) {
+  __shared__ int win_s[kRouteWarps][kRouteWindow];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  for (int t = blockIdx.x * kRouteWarps + w; t < T; t += gridDim.x * kRouteWarps) {
     int e;
     float g;
-    route_row_64(logits + static_cast<long long>(t) * ld, N, k, cfg, bias, lane, e, g);
+    route_row_64(x, t, N, k, cfg, bias, win_s[w], lane, e, g);
     if (lane < k) {
       idx[static_cast<long long>(t) * k + lane] = e;
       gates[static_cast<long long>(t) * k + lane] = g;
