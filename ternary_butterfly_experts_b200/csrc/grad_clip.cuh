@@ -11,19 +11,43 @@
 
 namespace bfmoe {
 
+//
+// Streaming: a producer warp walks the list in chunks and copies each
+// into a ring in shared memory (bulk copies), 16 consumer warps take them from
+// there, so that loads are in flight while the list is searched and squares
+// are summed.  (With loads into registers, 4 blocks of 512 threads an SM and
+// four 16-byte loads a thread, the norm of 189 MB of bfloat16 took 47 us, half
+// of the copy bandwidth: between a block's chunks nothing was in flight.)
 constexpr int kGradsPerLaunch = 512;
-constexpr int kGradThreads = 512;
-constexpr int kGradChunk = 8192;      // elements of a block's step
-constexpr int kGradMaxParts = 1024;   // partial sums of one call
+constexpr int kGradConsumers = 512;
+constexpr int kGradThreads = kGradConsumers + 32;
+constexpr int kGradBlocks = 2;          // of an SM
+// A chunk costs a block about 0.5 us besides its bytes: 189 MB of bfloat16 took
+// 51 us in chunks of 16 KB, 43 us in chunks of 32 KB, the same in 48 KB.
+constexpr int kGradChunkBytes = 32768;
+constexpr int kGradStages = 3;          // chunks of a block on their way or in work
+constexpr int kGradSmem = kGradStages * kGradChunkBytes;
+constexpr int kGradMaxParts = 1024;     // partial sums of one call
 
+// A tensor is cut at 16-byte boundaries: its first chunk has up to 15 bytes
+// before the first one too (head elements), its last less than 16 bytes more.
 struct GradList {
   const void* src[kGradsPerLaunch];
   void* dst[kGradsPerLaunch];
   long long len[kGradsPerLaunch];
   int first[kGradsPerLaunch + 1];  // chunks before each tensor
-  uint8_t src_type[kGradsPerLaunch], dst_type[kGradsPerLaunch];
+  uint8_t src_type[kGradsPerLaunch], dst_type[kGradsPerLaunch], head[kGradsPerLaunch];
   int n;
 };
+
+inline int grad_head(const void* p, int type, long long len) {
+  const int bytes = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15);
+  return static_cast<int>(std::min<long long>(bytes / (type == BFMOE_BF16 ? 2 : 4), len));
+}
+inline long long grad_chunks(const void* p, int type, long long len) {
+  const long long body = (len - grad_head(p, type, len)) * (type == BFMOE_BF16 ? 2 : 4);
+  return std::max(1LL, (body + kGradChunkBytes - 1) / kGradChunkBytes);
+}
 
 // The tensor of chunk c: the last i with first[i] <= c.
 __device__ __forceinline__ int grad_of_chunk(const GradList& g, int c) {
@@ -36,82 +60,308 @@ __device__ __forceinline__ int grad_of_chunk(const GradList& g, int c) {
   return lo;
 }
 
-__device__ __forceinline__ double block_sum(double v, double* red) {
-  v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  double s = 0.0;
-  if (threadIdx.x < 32) {
-    s = threadIdx.x < blockDim.x / 32 ? red[threadIdx.x] : 0.0;
-    s = warp_sum(s);
+// A chunk of a tensor: `vecs` 16-byte vectors from element `at` on are in
+// shared memory; `head` elements before `at` and `tail` behind them are not.
+struct GradChunk {
+  const void* src;
+  void* dst;
+  long long at;
+  int vecs;
+  uint8_t src_bf16, dst_bf16, head, tail;
+};
+
+// Chunks first, first + step, ... (count of them) through the ring.  The
+// consumer threads call ready() once, while the first copies are on their way;
+// where it says so use(chunk, vectors) for every chunk, else the copies stop
+// there.  Every wait is bounded; after one that ran out all return, the
+// producer after its own copies.
+template <class R, class F>
+__device__ __forceinline__ void grad_stream(const GradList& g, int first, int step, int count, R&& ready, F&& use) {
+  extern __shared__ __align__(128) uint8_t grad_ring[];
+  __shared__ uint64_t full[kGradStages], empty[kGradStages], go;
+  __shared__ GradChunk meta[kGradStages];
+  __shared__ int going;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kGradStages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, kGradConsumers / 32);
+    }
+    mbar_init(&go, 1);
+    mbar_fence_init();
   }
-  return s;  // valid in warp 0
-}
-
-__device__ __forceinline__ float grad_load(const void* p, int type, long long i) {
-  return type == BFMOE_BF16 ? to_f32(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
-}
-
-__global__ __launch_bounds__(kGradThreads) void grad_norm_kernel(const __grid_constant__ GradList g,
-                                                                 double* __restrict__ part) {
-  __shared__ double red[32];
-  double s = 0.0;
-  const int chunks = g.first[g.n];
-  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const int i = grad_of_chunk(g, c);
-    const long long a = static_cast<long long>(c - g.first[i]) * kGradChunk;
-    const long long b = min(a + kGradChunk, g.len[i]);
-    for (long long q = a + threadIdx.x; q < b; q += blockDim.x) {
-      const double v = static_cast<double>(grad_load(g.src[i], g.src_type[i], q));
-      s += v * v;
+  __syncthreads();
+  // chunk q goes through stage s for the turn-th time
+  constexpr int stages = kGradStages;
+  int s = 0, turn = 0;
+  auto next = [&] {
+    if (++s == stages) {
+      s = 0;
+      ++turn;
+    }
+  };
+  if (threadIdx.x >= kGradConsumers) {
+    if (threadIdx.x == kGradConsumers) {
+      int q = 0;
+      bool done = false;
+      // the tensor at hand: its list entry is read once
+      int c0 = 0, c1 = 0, sh = 0, head = 0;
+      long long len = 0;
+      GradChunk m{};
+      for (; q < count; ++q, next()) {
+        const int c = first + q * step;
+        if (c < c0 || c >= c1) {
+          const int i = grad_of_chunk(g, c);
+          c0 = g.first[i];
+          c1 = g.first[i + 1];
+          len = g.len[i];
+          head = g.head[i];
+          m.src = g.src[i];
+          m.dst = g.dst[i];
+          m.src_bf16 = g.src_type[i] == BFMOE_BF16;
+          m.dst_bf16 = g.dst_type[i] == BFMOE_BF16;
+          sh = m.src_bf16 ? 1 : 2;  // bytes of an element, as a shift
+        }
+        const int chunk = kGradChunkBytes >> sh;
+        m.at = head + static_cast<long long>(c - c0) * chunk;
+        const int n = static_cast<int>(min(len - m.at, static_cast<long long>(chunk)));
+        m.vecs = n >> (4 - sh);
+        m.head = static_cast<uint8_t>(c == c0 ? head : 0);
+        m.tail = static_cast<uint8_t>(n - (m.vecs << (4 - sh)));
+        if (q == stages) {
+          done = mbar_wait(&go, 0, 0x2203u) ? !going : true;
+          if (done) break;
+        }
+        if (turn > 0 && !mbar_wait(empty + s, (turn - 1) & 1, 0x2200u | s)) {
+          done = true;
+          break;
+        }
+        meta[s] = m;
+        mbar_expect_tx(full + s, m.vecs * 16);
+        if (m.vecs > 0)
+          bulk_load(grad_ring + s * kGradChunkBytes, static_cast<const uint8_t*>(m.src) + (m.at << sh), m.vecs * 16,
+                    full + s);
+      }
+      // the copies in flight where nobody takes them any more
+      if (q <= stages && !done) done = mbar_wait(&go, 0, 0x2204u) ? !going : true;
+      if (done)
+        for (int p = max(0, q - stages); p < q; ++p) mbar_wait(full + p % stages, (p / stages) & 1, 0x2201u);
+    }
+  } else {
+    const bool on = ready();
+    if (threadIdx.x == 0) {
+      going = on;
+      mbar_arrive(&go);
+    }
+    for (int q = 0; on && q < count; ++q, next()) {
+      if (__any_sync(FULL_MASK, !mbar_wait(full + s, turn & 1, 0x2202u | s))) break;
+      const GradChunk m = meta[s];
+      use(m, reinterpret_cast<const uint4*>(grad_ring + s * kGradChunkBytes));
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(empty + s);
     }
   }
-  s = block_sum(s, red);
-  if (threadIdx.x == 0) part[blockIdx.x] = s;
+  __syncthreads();
+}
+
+// Sum over the consumer threads (or a block of as many); valid in warp 0.
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"r"(kGradConsumers) : "memory"); }
+__device__ __forceinline__ double consumer_sum(double v, double* red) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  consumer_sync();
+  return threadIdx.x < 32 ? warp_sum(threadIdx.x < kGradConsumers / 32 ? red[threadIdx.x] : 0.0) : 0.0;
+}
+
+// 16 bytes of a tensor as float32.
+template <typename T>
+constexpr int kGradVec = 16 / sizeof(T);
+template <typename T>
+__device__ __forceinline__ void grad_unpack(const uint4& u, float (&v)[kGradVec<T>]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      v[i] = __uint_as_float(w[i]);
+    } else {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+
+__device__ __forceinline__ void add_square(double& s, float x) {
+  const double v = static_cast<double>(x);
+  s = fma(v, v, s);
+}
+
+// The squares of a vector.  bfloat16 becomes float64 without the conversion
+// unit (16 a clock and SM, half of what memory delivers): |x|'s bits moved to a
+// float64's are x 2^-896, zero and subnormal numbers included, and one product
+// with 2^896 makes them x.  Infinities and NaN come out finite: top, the
+// largest |x| of the two halves as integers, tells of them.
+template <typename T>
+__device__ __forceinline__ void square_vector(double (&s)[4], uint32_t& top, const uint4& u) {
+  if constexpr (sizeof(T) == 4) {
+    float f[4];
+    grad_unpack<T>(u, f);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) add_square(s[q], f[q]);
+  } else {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const double a = __hiloint2double(static_cast<int>((w[q] << 13) & 0x0fffe000u), 0) * 0x1p896;
+      const double b = __hiloint2double(static_cast<int>((w[q] >> 3) & 0x0fffe000u), 0) * 0x1p896;
+      s[q] = fma(a, a, s[q]);
+      s[q ^ 1] = fma(b, b, s[q ^ 1]);
+    }
+    top = __vimax3_u16x2(top, w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu);
+    top = __vimax3_u16x2(top, w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu);
+  }
+}
+
+__global__ __launch_bounds__(kGradThreads, kGradBlocks) void grad_norm_kernel(const __grid_constant__ GradList g,
+                                                                              double* __restrict__ part) {
+  __shared__ double red[32];
+  pdl_wait();
+  pdl_trigger();
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
+  uint32_t top = 0;
+  const int chunks = g.first[g.n];
+  const int mine = (chunks - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+  grad_stream(g, blockIdx.x, gridDim.x, mine, [] { return true; }, [&](const GradChunk& m, const uint4* v) {
+    const bool bf16 = m.src_bf16;
+    if (bf16) {
+#pragma unroll 4
+      for (int i = threadIdx.x; i < m.vecs; i += kGradConsumers) square_vector<__nv_bfloat16>(s, top, v[i]);
+    } else {
+#pragma unroll 4
+      for (int i = threadIdx.x; i < m.vecs; i += kGradConsumers) square_vector<float>(s, top, v[i]);
+    }
+    if (static_cast<int>(threadIdx.x) < m.head + m.tail) {
+      const int r = threadIdx.x;
+      const long long at = r < m.head ? r : m.at + static_cast<long long>(m.vecs) * (bf16 ? 8 : 4) + (r - m.head);
+      add_square(s[0], bf16 ? to_f32(static_cast<const __nv_bfloat16*>(m.src)[at])
+                            : static_cast<const float*>(m.src)[at]);
+    }
+  });
+  if (threadIdx.x >= kGradConsumers) return;
+  const uint32_t t = max(top & 0xffffu, top >> 16);
+  if (t >= 0x7f80u) s[0] += static_cast<double>(__uint_as_float(t << 16));  // infinity or NaN
+  const double sum = consumer_sum((s[0] + s[1]) + (s[2] + s[3]), red);
+  if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
 __device__ __forceinline__ double grad_total(const double* __restrict__ part, int parts) {
   __shared__ double red[32];
   __shared__ double total;
   double s = 0.0;
-  for (int q = threadIdx.x; q < parts; q += blockDim.x) s += part[q];
-  s = block_sum(s, red);
+  for (int q = threadIdx.x; q < parts; q += kGradConsumers) s += part[q];
+  s = consumer_sum(s, red);
   if (threadIdx.x == 0) total = sqrt(s);
-  __syncthreads();
+  consumer_sync();
   return total;
 }
 
-__global__ __launch_bounds__(kGradThreads) void grad_norm_finish_kernel(const double* __restrict__ part, int parts,
+__global__ __launch_bounds__(kGradConsumers) void grad_norm_finish_kernel(const double* __restrict__ part, int parts,
                                                                         float* __restrict__ norm) {
+  pdl_wait();
+  pdl_trigger();
   const double v = grad_total(part, parts);
   if (threadIdx.x == 0) *norm = static_cast<float>(v);
 }
 
-__global__ __launch_bounds__(kGradThreads) void grad_scale_kernel(const __grid_constant__ GradList g,
-                                                                  const double* __restrict__ part, int parts,
-                                                                  float max_norm, float* __restrict__ norm) {
-  const double v = grad_total(part, parts);
-  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(v);
-  const bool clip = v > static_cast<double>(max_norm) && v < INFINITY;
-  // a factor below the normal float32 range is applied in two steps, the
-  // first an exact power of two, so that it keeps its 24 bits
-  double f = static_cast<double>(max_norm) / v;
-  const float first = f < 0x1p-100 ? 0x1p-80f : 1.f;
-  if (f < 0x1p-100) f *= 0x1p80;
-  const float by = clip ? static_cast<float>(f) : 1.f;
-  const int chunks = g.first[g.n];
-  for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const int i = grad_of_chunk(g, c);
-    if (!clip && g.src[i] == g.dst[i]) continue;
-    const long long a = static_cast<long long>(c - g.first[i]) * kGradChunk;
-    const long long b = min(a + kGradChunk, g.len[i]);
-    for (long long q = a + threadIdx.x; q < b; q += blockDim.x) {
-      const float x = grad_load(g.src[i], g.src_type[i], q);
-      const float y = clip ? x * first * by : x;
-      if (g.dst_type[i] == BFMOE_BF16) static_cast<__nv_bfloat16*>(g.dst[i])[q] = __float2bfloat16_rn(y);
-      else static_cast<float*>(g.dst[i])[q] = y;
+struct GradFactor {
+  float first, by;  // applied one after the other
+  bool on;
+  __device__ __forceinline__ float operator()(float x) const { return on ? x * first * by : x; }
+};
+
+template <typename Td>
+__device__ __forceinline__ void grad_store(Td* p, const float* v, int n) {
+  if constexpr (sizeof(Td) == 4) {
+#pragma unroll
+    for (int q = 0; q < n; q += 4) __stcs(reinterpret_cast<float4*>(p + q), make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]));
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < n / 2; ++q) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * q], v[2 * q + 1]);
+      w[q] = *reinterpret_cast<const uint32_t*>(&b);
     }
+    if (n == 8) __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+    else __stcs(reinterpret_cast<uint2*>(p), make_uint2(w[0], w[1]));
   }
+}
+
+// A chunk from shared memory to d times f.  Wide where the output reaches a
+// boundary together with the tensor (always when they are the same).
+template <typename T, typename Td>
+__device__ __forceinline__ void grad_scale_chunk(const GradChunk& m, const uint4* v, const T* p, Td* d, const GradFactor& f) {
+  constexpr int VE = kGradVec<T>;
+  constexpr size_t WANT = VE * sizeof(Td) < 16 ? VE * sizeof(Td) : 16;
+  Td* out = d + m.at;
+  if ((reinterpret_cast<uintptr_t>(out) & (WANT - 1)) == 0) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < m.vecs; i += kGradConsumers) {
+      float x[VE];
+      grad_unpack<T>(v[i], x);
+#pragma unroll
+      for (int q = 0; q < VE; ++q) x[q] = f(x[q]);
+      grad_store(out + static_cast<size_t>(i) * VE, x, VE);
+    }
+  } else {
+    const T* e = reinterpret_cast<const T*>(v);
+    for (int i = threadIdx.x; i < m.vecs * VE; i += kGradConsumers) out[i] = from_f32<Td>(f(to_f32(e[i])));
+  }
+  if (static_cast<int>(threadIdx.x) < m.head + m.tail) {
+    const int r = threadIdx.x;
+    const long long at = r < m.head ? r : m.at + static_cast<long long>(m.vecs) * VE + (r - m.head);
+    d[at] = from_f32<Td>(f(to_f32(p[at])));
+  }
+}
+
+// The chunks are taken from the last one on: what the norm read last is still
+// in L2.
+__global__ __launch_bounds__(kGradThreads, kGradBlocks) void grad_scale_kernel(const __grid_constant__ GradList g,
+                                                                               const double* __restrict__ part,
+                                                                               int parts, int all_in_place,
+                                                                               float max_norm,
+                                                                               float* __restrict__ norm) {
+  // The copies start before the norm's kernel has ended: that kernel's blocks
+  // had all seen the gradients' writers end, and it writes none itself.
+  pdl_trigger();
+  GradFactor f{};
+  const int last = g.first[g.n] - 1 - static_cast<int>(blockIdx.x);
+  grad_stream(g, last, -static_cast<int>(gridDim.x), last / static_cast<int>(gridDim.x) + 1,
+              [&] {
+                pdl_wait();
+                const double v = grad_total(part, parts);
+                if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(v);
+                f.on = v > static_cast<double>(max_norm) && v < INFINITY;
+                // a factor below the normal float32 range is applied in two
+                // steps, the first an exact power of two, to keep its 24 bits
+                double by = static_cast<double>(max_norm) / v;
+                f.first = by < 0x1p-100 ? 0x1p-80f : 1.f;
+                if (by < 0x1p-100) by *= 0x1p80;
+                f.by = static_cast<float>(by);
+                return f.on || !all_in_place;
+              },
+              [&](const GradChunk& m, const uint4* vec) {
+                const void* p = m.src;
+                void* d = m.dst;
+                if (!f.on && p == d) return;
+                const bool to_bf16 = m.dst_bf16;
+                if (m.src_bf16) {
+                  const auto* x = static_cast<const __nv_bfloat16*>(p);
+                  if (to_bf16) grad_scale_chunk(m, vec, x, static_cast<__nv_bfloat16*>(d), f);
+                  else grad_scale_chunk(m, vec, x, static_cast<float*>(d), f);
+                } else {
+                  const auto* x = static_cast<const float*>(p);
+                  if (to_bf16) grad_scale_chunk(m, vec, x, static_cast<__nv_bfloat16*>(d), f);
+                  else grad_scale_chunk(m, vec, x, static_cast<float*>(d), f);
+                }
+              });
 }
 
 }  // namespace bfmoe

@@ -29,12 +29,12 @@ using namespace bfmoe;
 
 namespace {
 
-// Blocks of the loss kernel, which leaves one row of partial sums each.
-constexpr int kBalanceBlocks = 296;
+// Blocks of the loss kernel at most, which leaves one row of partial sums each.
+constexpr int kBalanceBlocks = 320;
 
 struct RoutePlan {
   size_t chunk_counts, totals;  // buckets
-  size_t part, zpart;           // balance loss
+  size_t part, zpart, loads;    // balance loss
   size_t total;
 };
 
@@ -54,6 +54,7 @@ RoutePlan make_route_plan(int N, long long T, int k) {
   off = 0;
   p.part = take(static_cast<size_t>(kBalanceBlocks) * N * 4);
   p.zpart = take(static_cast<size_t>(kBalanceBlocks) * 8);
+  p.loads = take(static_cast<size_t>(kBalanceBlocks) * (N + 1) * 4);
   p.total = std::max(buckets_end, off);
   return p;
 }
@@ -174,32 +175,52 @@ void fill_list(const bfmoe_grad* g, int i0, int i1, GradList& out) {
     out.src_type[q] = static_cast<uint8_t>(g[i].dtype);
     out.dst_type[q] = static_cast<uint8_t>(g[i].out ? g[i].out_dtype : g[i].dtype);
     out.first[q] = static_cast<int>(chunks);
-    chunks += (g[i].len + kGradChunk - 1) / kGradChunk;
+    out.head[q] = static_cast<uint8_t>(grad_head(g[i].grad, g[i].dtype, g[i].len));
+    chunks += grad_chunks(g[i].grad, g[i].dtype, g[i].len);
   }
   out.first[out.n] = static_cast<int>(chunks);
 }
 
 long long total_chunks(const bfmoe_grad* g, int n) {
   long long c = 0;
-  for (int i = 0; i < n; ++i) c += (g[i].len + kGradChunk - 1) / kGradChunk;
+  for (int i = 0; i < n; ++i)
+    if (g[i].len > 0) c += grad_chunks(g[i].grad, g[i].dtype, g[i].len);
   return c;
 }
 
 // The squares of the whole list into part; *parts: how many partial sums.
 int launch_norm(const char* what, const bfmoe_grad* g, int n, double* part, int* parts, cudaStream_t s) {
   *parts = 0;
+  static std::atomic<uint64_t> done{0};
+  if (needs_attr(done)) {
+    cudaError_t e = cudaFuncSetAttribute(grad_norm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(grad_scale_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem);
+    if (e != cudaSuccess) return cuda_fail(e, what);
+    attr_set(done);
+  }
   const int lists = (n + kGradsPerLaunch - 1) / kGradsPerLaunch;
-  const int cap = lists ? std::min(sm_count() * 4, kGradMaxParts / lists) : 0;
+  const int cap = lists ? std::min(sm_count() * kGradBlocks, kGradMaxParts / lists) : 0;
   GradList l;
   for (int q = 0; q < lists; ++q) {
     fill_list(g, q * kGradsPerLaunch, std::min(n, (q + 1) * kGradsPerLaunch), l);
     if (l.first[l.n] == 0) continue;
     const int grid = std::min(l.first[l.n], cap);
-    const cudaError_t e = launch("grad_norm", s, [&] { grad_norm_kernel<<<grid, kGradThreads, 0, s>>>(l, part + *parts); });
+    const cudaError_t e = launch("grad_norm", s, [&] { pdl_launch(grad_norm_kernel, grid, kGradThreads, kGradSmem, s, l, part + *parts); });
     if (e != cudaSuccess) return cuda_fail(e, what);
     *parts += grid;
   }
   return BFMOE_OK;
+}
+
+// Calls f with the shape that rows of N <= 1024 experts take.
+template <class F>
+cudaError_t with_shape(int N, F&& f) {
+  if (N <= 64) return f(RowShape<16, 4>{});
+  if (N <= 128) return f(RowShape<16, 8>{});
+  if (N <= 256) return f(RowShape<32, 8>{});
+  if (N <= 512) return f(RowShape<32, 16>{});
+  return f(RowShape<32, 32>{});
 }
 
 template <class S, int BY, bool GROUPED>
@@ -209,13 +230,13 @@ cudaError_t launch_route_rows(Logits x, int T, int N, int k, const RouteCfg& cfg
   while (GROUPED && (2 << lsh) * cfg.n_groups <= S::LPR) ++lsh;
   x.wide = wide_rows<S>(x.p, x.ld, N, x.bf16 != 0);
   const size_t floats = (BY != kByLogit ? S::MAXN : 0) + (GROUPED ? kRouteWarps * S::ROWS * kGroupSpace<S> : 0) +
-                        (S::V > 8 && x.wide ? kRouteWarps * 2 * S::MAXN : 0);
+                        (x.wide ? kRouteWarps * RowFeed<S>::BUFFER / 4 : 0);
   if (S::V > 8) {
     static std::atomic<uint64_t> done{0};
     if (needs_attr(done)) {
       const cudaError_t e = cudaFuncSetAttribute(route_fast_kernel<S, BY, GROUPED>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (1 + kRouteWarps + 2 * kRouteWarps) * S::MAXN * 4);
+                                                 S::MAXN * 4 + kRouteWarps * (S::ROWS * kGroupSpace<S> * 4 + RowFeed<S>::BUFFER));
       if (e != cudaSuccess) return e;
       attr_set(done);
     }
@@ -246,14 +267,86 @@ cudaError_t launch_route_shape(const Logits& x, int T, int N, int k, const Route
 // A row's logits in the registers of 16 or 32 lanes up to 1024 experts.
 cudaError_t launch_route(const Logits& x, int T, int N, int k, const RouteCfg& cfg, const float* bias, int32_t* idx,
                          float* gates, cudaStream_t s) {
-  if (N <= 64) return launch_route_shape<RowShape<16, 4>>(x, T, N, k, cfg, bias, idx, gates, s);
-  if (N <= 128) return launch_route_shape<RowShape<16, 8>>(x, T, N, k, cfg, bias, idx, gates, s);
-  if (N <= 256) return launch_route_shape<RowShape<32, 8>>(x, T, N, k, cfg, bias, idx, gates, s);
-  if (N <= 512) return launch_route_shape<RowShape<32, 16>>(x, T, N, k, cfg, bias, idx, gates, s);
-  if (N <= 1024) return launch_route_shape<RowShape<32, 32>>(x, T, N, k, cfg, bias, idx, gates, s);
+  if (N <= 1024)
+    return with_shape(
+        N, [&](auto shape) { return launch_route_shape<decltype(shape)>(x, T, N, k, cfg, bias, idx, gates, s); });
   return launch("route", s, [&] {
     route_long_kernel<<<grid_for(T, kRouteWarps, sm_count() * 8), kRouteWarps * 32, 0, s>>>(x, T, N, k, cfg, bias, idx,
                                                                                             gates);
+  });
+}
+
+template <class S, bool SIGMOID>
+cudaError_t launch_balance_rows(Logits x, int T, int N, int k, const int32_t* idx, float* part, double* zpart,
+                                int32_t* loads, int* grid, cudaStream_t s) {
+  constexpr size_t most = std::max<size_t>(kGradWarps * S::MAXN * 4, kGradWarps * RowFeed<S>::BUFFER);
+  const auto kern = balance_rows_kernel<S, SIGMOID>;
+  static std::atomic<uint64_t> done{0};
+  if (needs_attr(done)) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+    if (e != cudaSuccess) return e;
+    attr_set(done);
+  }
+  x.wide = wide_rows<S>(x.p, x.ld, N, x.bf16 != 0);
+  // a warp takes several rows where there are enough, so that the sums that
+  // are left to add up stay few
+  *grid = grid_for(T, kGradWarps * S::ROWS * 2, std::min(kBalanceBlocks, sm_count() * 2));
+  return launch("balance_rows", s, [&] {
+    pdl_launch(kern, *grid, kGradWarps * 32, most, s, x, T, N, k, idx, part, zpart, loads);
+  });
+}
+
+cudaError_t launch_balance(Logits x, int T, int N, int k, bool sigmoid, const int32_t* idx, float* part, double* zpart,
+                           int32_t* loads, int* grid, cudaStream_t s) {
+  if (N <= 1024)
+    return with_shape(N, [&](auto shape) {
+      using S = decltype(shape);
+      if (sigmoid) return launch_balance_rows<S, true>(x, T, N, k, idx, part, zpart, loads, grid, s);
+      return launch_balance_rows<S, false>(x, T, N, k, idx, part, zpart, loads, grid, s);
+    });
+  static std::atomic<uint64_t> done{0};
+  if (needs_attr(done)) {
+    const cudaError_t e = cudaFuncSetAttribute(balance_long_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (kGradWarps + 1) * BFMOE_MAX_EXPERTS * 4);
+    if (e != cudaSuccess) return e;
+    attr_set(done);
+  }
+  *grid = grid_for(T, kGradWarps, std::min(kBalanceBlocks, sm_count() * 2));
+  return launch("balance_rows", s, [&] {
+    pdl_launch(balance_long_kernel, *grid, kGradWarps * 32, static_cast<size_t>(kGradWarps + 1) * N * 4, s, x, T, N, k,
+               sigmoid ? 1 : 0, idx, part, zpart, loads);
+  });
+}
+
+template <class S, bool SIGMOID>
+cudaError_t launch_backward_rows(Logits x, int T, int N, int k, const RouteCfg& cfg, RouteGrad g, cudaStream_t s) {
+  constexpr size_t base = S::MAXN * (1 + kGradWarps * S::ROWS) * 4, most = base + kGradWarps * RowFeed<S>::BUFFER;
+  const auto kern = route_backward_kernel<S, SIGMOID>;
+  static std::atomic<uint64_t> done{0};
+  if (needs_attr(done)) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+    if (e != cudaSuccess) return e;
+    attr_set(done);
+  }
+  x.wide = wide_rows<S>(x.p, x.ld, N, x.bf16 != 0);
+  g.wide_out = wide_rows<S>(g.out, g.ld_out, N, x.bf16 != 0);
+  const int grid = grid_for(T, kGradWarps * S::ROWS, sm_count() * kGradRowBlocks<S>);
+  return launch("route_backward", s, [&] {
+    pdl_launch(kern, grid, kGradWarps * 32, x.wide ? most : base, s, x, T, N, k, cfg, g);
+  });
+}
+
+cudaError_t launch_route_backward(Logits x, int T, int N, int k, const RouteCfg& cfg, const RouteGrad& g,
+                                  cudaStream_t s) {
+  if (N <= 1024)
+    return with_shape(N, [&](auto shape) {
+      using S = decltype(shape);
+      if (cfg.score == BFMOE_SCORE_SIGMOID) return launch_backward_rows<S, true>(x, T, N, k, cfg, g, s);
+      return launch_backward_rows<S, false>(x, T, N, k, cfg, g, s);
+    });
+  return launch("route_backward", s, [&] {
+    pdl_launch(route_backward_long_kernel, grid_for(T, kGradWarps, sm_count() * 8), kGradWarps * 32, 0, s, x, T, N, k,
+               cfg, g);
   });
 }
 
@@ -322,27 +415,15 @@ int bfmoe_balance_loss(const void* logits, int dtype, int T, long long ld, int n
   uint8_t* W = static_cast<uint8_t*>(ws);
   float* part = reinterpret_cast<float*>(W + p.part);
   double* zpart = reinterpret_cast<double*>(W + p.zpart);
-  if ((e = cudaMemsetAsync(load, 0, sizeof(int32_t) * (N + 1), s)) != cudaSuccess) return cuda_fail(e, "balance_loss: memset");
-  const int grid = std::min(kBalanceBlocks, grid_for(T, kGradWarps, kBalanceBlocks));
-  const size_t smem = static_cast<size_t>(kGradWarps) * N * sizeof(float);
-  static std::atomic<uint64_t> done{0};
-  if (needs_attr(done)) {
-    const int most = kGradWarps * BFMOE_MAX_EXPERTS * 4;
-    if ((e = cudaFuncSetAttribute(balance_rows_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(balance_rows_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess)
-      return cuda_fail(e, "balance_loss: attribute");
-    attr_set(done);
-  }
-  e = launch("balance_rows", s, [&] {
-    if (dtype == BFMOE_BF16)
-      balance_rows_kernel<<<grid, kGradWarps * 32, smem, s>>>(static_cast<const __nv_bfloat16*>(logits), ld, T, N, k,
-                                                              score, idx, part, zpart, load);
-    else
-      balance_rows_kernel<<<grid, kGradWarps * 32, smem, s>>>(static_cast<const float*>(logits), ld, T, N, k, score,
-                                                              idx, part, zpart, load);
-  });
+  int32_t* loads = reinterpret_cast<int32_t*>(W + p.loads);
+  int grid = 0;
+  e = launch_balance(Logits{logits, ld, dtype == BFMOE_BF16, 0}, T, N, k, score == BFMOE_SCORE_SIGMOID, idx, part, zpart,
+                     loads, &grid, s);
   if (e != cudaSuccess) return cuda_fail(e, "balance_loss: launch");
-  e = launch("balance_finish", s, [&] { balance_finish_kernel<<<1, 1024, 0, s>>>(part, zpart, grid, N, k, load, loss); });
+  e = launch("balance_finish", s, [&] {
+    pdl_launch(balance_finish_kernel, kFinishBlocks, kFinishThreads, 0, s, static_cast<const float*>(part),
+               static_cast<const double*>(zpart), static_cast<const int32_t*>(loads), grid, N, k, load, loss);
+  });
   if (e != cudaSuccess) return cuda_fail(e, "balance_loss: launch");
   return ok();
 }
@@ -363,17 +444,8 @@ int bfmoe_route_backward(const void* logits, int dtype, int T, long long ld, int
   if (logits == dlogits && ld != ld_dlogits) return fail(BFMOE_EINVAL, "route_backward: in place with another row stride");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const RouteCfg cfg = cfg_of(scoring);
-  const int grid = grid_for(T, kGradWarps, sm_count() * 8);
-  const cudaError_t e = launch("route_backward", s, [&] {
-    if (dtype == BFMOE_BF16)
-      route_backward_kernel<<<grid, kGradWarps * 32, 0, s>>>(static_cast<const __nv_bfloat16*>(logits), ld, T, N, k,
-                                                             cfg, idx, dgates, load, dloss,
-                                                             static_cast<__nv_bfloat16*>(dlogits), ld_dlogits);
-    else
-      route_backward_kernel<<<grid, kGradWarps * 32, 0, s>>>(static_cast<const float*>(logits), ld, T, N, k, cfg, idx,
-                                                             dgates, load, dloss, static_cast<float*>(dlogits),
-                                                             ld_dlogits);
-  });
+  const RouteGrad g{idx, dgates, load, dloss, dlogits, ld_dlogits, 0};
+  const cudaError_t e = launch_route_backward(Logits{logits, ld, dtype == BFMOE_BF16, 0}, T, N, k, cfg, g, s);
   if (e != cudaSuccess) return cuda_fail(e, "route_backward: launch");
   return ok();
 }
@@ -390,7 +462,7 @@ int bfmoe_grad_norm(const bfmoe_grad* grads, int n, float* norm, void* ws, size_
   double* part = static_cast<double*>(ws);
   int parts = 0;
   if ((rc = launch_norm("grad_norm: launch", grads, n, part, &parts, s))) return rc;
-  const cudaError_t e = launch("grad_norm_finish", s, [&] { grad_norm_finish_kernel<<<1, kGradThreads, 0, s>>>(part, parts, norm); });
+  const cudaError_t e = launch("grad_norm_finish", s, [&] { pdl_launch(grad_norm_finish_kernel, 1, kGradConsumers, 0, s, part, parts, norm); });
   if (e != cudaSuccess) return cuda_fail(e, "grad_norm: launch");
   return ok();
 }
@@ -414,13 +486,15 @@ int bfmoe_grad_clip(const bfmoe_grad* grads, int n, float max_norm, float* norm,
   for (int i0 = 0; i0 < n; i0 += kGradsPerLaunch) {
     fill_list(grads, i0, std::min(n, i0 + kGradsPerLaunch), l);
     if (l.first[l.n] == 0) continue;
-    const int grid = std::min(l.first[l.n], sm_count() * 4);
-    e = launch("grad_scale", s, [&] { grad_scale_kernel<<<grid, kGradThreads, 0, s>>>(l, part, parts, max_norm, out_norm); });
+    int in_place = 1;
+    for (int q = 0; q < l.n; ++q) in_place &= l.src[q] == l.dst[q];
+    const int grid = std::min(l.first[l.n], sm_count() * kGradBlocks);
+    e = launch("grad_scale", s, [&] { pdl_launch(grad_scale_kernel, grid, kGradThreads, kGradSmem, s, l, part, parts, in_place, max_norm, out_norm); });
     if (e != cudaSuccess) return cuda_fail(e, "grad_clip: launch");
     out_norm = nullptr;  // written once
   }
   if (out_norm) {  // nothing to scale: the norm of an empty list
-    e = launch("grad_norm_finish", s, [&] { grad_norm_finish_kernel<<<1, kGradThreads, 0, s>>>(part, parts, norm); });
+    e = launch("grad_norm_finish", s, [&] { pdl_launch(grad_norm_finish_kernel, 1, kGradConsumers, 0, s, part, parts, norm); });
     if (e != cudaSuccess) return cuda_fail(e, "grad_clip: launch");
   }
   return ok();

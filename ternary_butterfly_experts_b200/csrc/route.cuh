@@ -458,6 +458,81 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+// A warp's rows t0, t0 + step, ..., loads ahead of the work: rows of up to 256
+// experts as registers, longer ones (in cells) through two buffers of the warp
+// in shared memory.
+template <class S>
+struct RowFeed {
+  static constexpr bool AHEAD = S::V <= 8;
+  static constexpr int BUFFER = AHEAD ? 0 : 2 * S::MAXN * 4;  // bytes of shared memory of a warp
+  RawRow<S> raw;
+  uint8_t* buf;
+  uint64_t* full;
+  const uint8_t* here;  // the row in shared memory, or NULL
+  int turn;
+  bool staged;
+
+  __device__ __forceinline__ void fetch(const Logits& x, int t, int N, int b) {  // one lane
+    const int es = x.bf16 ? 2 : 4;
+    mbar_expect_tx(full + b, N * es);
+    bulk_load(buf + b * S::MAXN * 4, static_cast<const uint8_t*>(x.p) + static_cast<long long>(t) * x.ld * es, N * es,
+              full + b);
+  }
+  // bars: two of the warp's (not AHEAD)
+  __device__ __forceinline__ void start(const Logits& x, int t0, int T, int N, int lane, uint8_t* buffer, uint64_t* bars) {
+    here = nullptr;
+    turn = 0;
+    staged = !AHEAD && x.wide;
+    buf = buffer;
+    full = bars;
+    if constexpr (AHEAD) {
+      if (t0 < T) raw.load(x, min(t0 + lane / S::LPR, T - 1), N, lane & (S::LPR - 1));
+    } else if (staged) {
+      if (lane == 0) {
+        mbar_init(full, 1);
+        mbar_init(full + 1, 1);
+        mbar_fence_init();
+        if (t0 < T) fetch(x, t0, N, 0);
+      }
+      __syncwarp();
+    }
+  }
+  // The logits of the warp's rows at t0 (a row past the end: the last one's).
+  // False after a copy that did not come, which is reported: then nothing of
+  // the warp's is on its way any more.
+  __device__ __forceinline__ bool take(const Logits& x, int t0, int step, int T, int N, int lane, float (&l)[S::V]) {
+    const int q = lane & (S::LPR - 1);
+    if constexpr (AHEAD) {
+      raw.unpack(x.bf16, l);
+      if (t0 + step < T) raw.load(x, min(t0 + step + lane / S::LPR, T - 1), N, q);
+    } else {
+      if (staged) {
+        const int b = turn & 1;
+        // the buffer of the row before was read before that row's work
+        if (lane == 0 && t0 + step < T) fetch(x, t0 + step, N, b ^ 1);
+        if (__any_sync(FULL_MASK, !mbar_wait(full + b, (turn >> 1) & 1, 0x2100u))) {
+          if (t0 + step < T) mbar_wait(full + (b ^ 1), ((turn + 1) >> 1) & 1, 0x2101u);
+          return false;
+        }
+        here = buf + b * S::MAXN * 4;
+        raw.load_shared(here, x.bf16, N, q);
+        __syncwarp();
+        ++turn;
+      } else {
+        raw.load(x, min(t0 + lane / S::LPR, T - 1), N, q);
+      }
+      raw.unpack(x.bf16, l);
+    }
+    return true;
+  }
+  // Logit e of row t, the row taken last.
+  __device__ __forceinline__ float at(const Logits& x, int t, int e) const {
+    if (!AHEAD && here)
+      return x.bf16 ? to_f32(reinterpret_cast<const __nv_bfloat16*>(here)[e]) : reinterpret_cast<const float*>(here)[e];
+    return x.at(t, e);
+  }
+};
+
 // exp(l - m) of a row and its sum over the row; masked logits give 0.
 template <class S>
 __device__ __forceinline__ float row_softmax(const float (&l)[S::V], float m, float (&u)[S::V]) {
@@ -541,58 +616,18 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
 
   const int step = gridDim.x * kRouteWarps * S::ROWS;
   int t0 = (blockIdx.x * kRouteWarps + w) * S::ROWS;
-  // Loads run ahead: rows of up to 256 experts as registers, longer ones (in
-  // cells) through two buffers of the warp in shared memory.
-  constexpr bool AHEAD = V <= 8;
-  __shared__ uint64_t full_s[AHEAD ? 1 : kRouteWarps * 2];
-  const bool staged = !AHEAD && x.wide;
-  const uint32_t row_bytes = static_cast<uint32_t>(N) * (x.bf16 ? 2u : 4u);
-  uint8_t* buf = reinterpret_cast<uint8_t*>(route_smem + (SCORED ? S::MAXN : 0) +
-                                            (GROUPED ? kRouteWarps * S::ROWS * kGroupSpace<S> : 0)) +
-                 static_cast<size_t>(w) * 2 * S::MAXN * 4;
-  uint64_t* full = full_s + w * 2;
-  auto fetch = [&](int tn, int b) {  // lane 0: row tn into buffer b
-    mbar_expect_tx(full + b, row_bytes);
-    bulk_load(buf + b * S::MAXN * 4,
-              static_cast<const uint8_t*>(x.p) + static_cast<long long>(tn) * x.ld * (x.bf16 ? 2 : 4), row_bytes, full + b);
-  };
-  int turn = 0;  // rows this warp has taken
-  if (staged) {
-    if (lane == 0) {
-      mbar_init(full, 1);
-      mbar_init(full + 1, 1);
-      mbar_fence_init();
-      if (t0 < T) fetch(t0, 0);
-    }
-    __syncwarp();
-  }
-  RawRow<S> raw;
-  if (AHEAD && t0 < T) raw.load(x, min(t0 + lane / LPR, T - 1), N, q);
+  __shared__ uint64_t full_s[kRouteWarps * 2];
+  RowFeed<S> feed;
+  feed.start(x, t0, T, N, lane,
+             reinterpret_cast<uint8_t*>(route_smem + (SCORED ? S::MAXN : 0) +
+                                        (GROUPED ? kRouteWarps * S::ROWS * kGroupSpace<S> : 0)) +
+                 static_cast<size_t>(w) * RowFeed<S>::BUFFER,
+             full_s + w * 2);
   for (; t0 < T; t0 += step) {
     const int t = min(t0 + lane / LPR, T - 1);
     const bool has = t0 + lane / LPR < T;
     float l[V], c[V];
-    const uint8_t* here = nullptr;  // the row in shared memory
-    if constexpr (!AHEAD) {
-      if (staged) {
-        const int b = turn & 1;
-        // the buffer of the row before was read before that row's picks
-        if (lane == 0 && t0 + step < T) fetch(t0 + step, b ^ 1);
-        // a copy that does not come is reported; every lane sees the same
-        if (__any_sync(FULL_MASK, !mbar_wait(full + b, (turn >> 1) & 1, 0x2100u))) {
-          if (t0 + step < T) mbar_wait(full + (b ^ 1), ((turn + 1) >> 1) & 1, 0x2101u);
-          return;
-        }
-        here = buf + b * S::MAXN * 4;
-        raw.load_shared(here, x.bf16, N, q);
-        __syncwarp();
-        ++turn;
-      } else {
-        raw.load(x, t, N, q);
-      }
-    }
-    raw.unpack(x.bf16, l);
-    if (AHEAD && t0 + step < T) raw.load(x, min(t0 + step + lane / LPR, T - 1), N, q);
+    if (!feed.take(x, t0, step, T, N, lane, l)) return;
     float m = 0.f, inv_z = 1.f;
     if constexpr (BY == kBySoftmax) {
       float h = l[0];
@@ -884,10 +919,7 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
       e = ((place / CE) * LPR + from) * CE + place % CE;
       live = q < n && (pick & ~LOW) > MASKED;
       if (live) {
-        if (!AHEAD && here)
-          le = x.bf16 ? to_f32(reinterpret_cast<const __nv_bfloat16*>(here)[e]) : reinterpret_cast<const float*>(here)[e];
-        else
-          le = x.at(t, e);
+        le = feed.at(x, t, e);
         if (bias || !cfg.renorm) sc = softmax ? unit_softmax(le, m) * inv_z : sigmoid_fast(le);
         val = le;
         eps = 0.f;

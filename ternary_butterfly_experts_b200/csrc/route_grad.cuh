@@ -17,21 +17,176 @@
 namespace bfmoe {
 
 constexpr int kGradWarps = 8;
+template <class S>
+constexpr int kGradRowBlocks = S::V <= 8 ? 4 : 2;  // of an SM
 
-// Sums of one row for the losses.
+// lse of a row from its largest logit and sum of exp(l - m).
+__device__ __forceinline__ float row_lse(float m, float z) { return m + __logf(z); }
+
+// e^-|l| and 1 / (1 + e^-|l|): sigmoid(l) and sigmoid(-l) without cancellation.
+struct TwoSided {
+  float s, t;  // sigmoid(l), sigmoid(-l)
+  __device__ __forceinline__ explicit TwoSided(float l) {
+    const float e = exp_fast(-fabsf(l)), r = rcp_fast(1.f + e);
+    s = l > 0.f ? r : e * r;
+    t = l > 0.f ? e * r : r;
+  }
+};
+// The row's sigmoids over exp(low) in u (low = min(m, 0)), and sigmoid(-l) in
+// t; masked logits give 0 and 1.
+template <class S>
+__device__ __forceinline__ void row_sigmoid(const float (&l)[S::V], float m, float (&u)[S::V], float (&t)[S::V]) {
+#pragma unroll
+  for (int i = 0; i < S::V; ++i) {
+    const TwoSided v(l[i]);
+    u[i] = v.s;
+    t[i] = v.t;
+  }
+  if (__any_sync(FULL_MASK, m < 0.f)) {
+    if (m < 0.f && m > -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < S::V; ++i) u[i] = masked_logit(l[i]) ? 0.f : exp_fast(l[i] - m) * t[i];
+    }
+  }
+}
+template <class S>
+__device__ __forceinline__ float row_max(const float (&l)[S::V]) {
+  float h = l[0];
+#pragma unroll
+  for (int i = 1; i < S::V; ++i) h = fmaxf(h, l[i]);
+  return seg_max<S::LPR>(h);
+}
+// Four values of a lane's cell from an array in shared memory.
+template <class S>
+__device__ __forceinline__ void load_cells(const float* a, int q, float (&v)[S::V]) {
+#pragma unroll
+  for (int c = 0; c < S::C; ++c)
+#pragma unroll
+    for (int h = 0; h < S::CE; h += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(a + (c * S::LPR + q) * S::CE + h);
+      v[c * S::CE + h] = f.x, v[c * S::CE + h + 1] = f.y, v[c * S::CE + h + 2] = f.z, v[c * S::CE + h + 3] = f.w;
+    }
+}
+
+// One pass over the logits: the sums of the losses' terms over this block's
+// rows, in a fixed order: part [grid][N] of p_te, zpart [grid] of lse^2, and
+// loads [grid][N + 1], the chosen slots of each expert and the rows.  A lane
+// keeps the sums of its experts in registers.
+template <class S, bool SIGMOID>
+__global__ __launch_bounds__(kGradWarps * 32, kGradRowBlocks<S>) void balance_rows_kernel(
+    const Logits x, int T, int N, int k, const int32_t* __restrict__ idx, float* __restrict__ part,
+    double* __restrict__ zpart, int32_t* __restrict__ loads) {
+  constexpr int LPR = S::LPR, V = S::V;
+  extern __shared__ __align__(128) float grad_smem[];  // sums of a warp [kGradWarps][MAXN]; during the rows: their buffers
+  __shared__ int hist[S::MAXN];
+  __shared__ double zs[kGradWarps];
+  __shared__ int rs[kGradWarps];
+  __shared__ uint64_t full_s[kGradWarps * 2];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, q = lane & (LPR - 1);
+  for (int e = threadIdx.x; e < S::MAXN; e += blockDim.x) hist[e] = 0;
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  float sum[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) sum[i] = 0.f;
+  double z2 = 0.0;
+  int rows = 0;
+  const int step = gridDim.x * kGradWarps * S::ROWS;
+  int t0 = (blockIdx.x * kGradWarps + w) * S::ROWS;
+  RowFeed<S> feed;
+  feed.start(x, t0, T, N, lane, reinterpret_cast<uint8_t*>(grad_smem) + static_cast<size_t>(w) * RowFeed<S>::BUFFER,
+             full_s + w * 2);
+  auto slot = [&](int t) { return q < k && t < T ? idx[static_cast<long long>(t) * k + q] : -1; };
+  int e = slot(t0 + lane / LPR);
+  for (; t0 < T; t0 += step) {
+    const int t = t0 + lane / LPR;
+    float l[V], u[V];
+    if (!feed.take(x, t0, step, T, N, lane, l)) break;
+    const int e_now = e;
+    e = slot(t + step);
+    const float m = row_max<S>(l);
+    const bool some = t < T && m > -INFINITY;
+    const float z = row_softmax<S>(l, m, u);
+    float inv;
+    if constexpr (SIGMOID) {
+      float c[V];
+      row_sigmoid<S>(l, m, u, c);
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) s += u[i];
+      inv = rcp_fast(seg_sum<LPR>(s));
+    } else {
+      inv = rcp_fast(z);
+    }
+    if (some) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum[i] = fmaf(u[i], inv, sum[i]);
+      if (q < k) {
+        if (e_now >= 0 && e_now < N) atomicAdd(hist + e_now, 1);
+        else report_error(BFMOE_EDEVICE_BOUNDS, static_cast<unsigned>(t));
+      }
+      if (q == 0) {
+        const double lse = static_cast<double>(row_lse(m, z));
+        z2 += lse * lse;
+        ++rows;
+      }
+    }
+  }
+  // lanes, then warps
+#pragma unroll
+  for (int o = LPR; o < 32; o <<= 1) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum[i] += __shfl_xor_sync(FULL_MASK, sum[i], o);
+    z2 += __shfl_xor_sync(FULL_MASK, z2, o);
+    rows += __shfl_xor_sync(FULL_MASK, rows, o);
+  }
+  __syncthreads();  // the row buffers are read
+  if (lane < LPR) {
+#pragma unroll
+    for (int c = 0; c < S::C; ++c)
+#pragma unroll
+      for (int h = 0; h < S::CE; h += 4)
+        *reinterpret_cast<float4*>(grad_smem + w * S::MAXN + (c * LPR + q) * S::CE + h) =
+            make_float4(sum[c * S::CE + h], sum[c * S::CE + h + 1], sum[c * S::CE + h + 2], sum[c * S::CE + h + 3]);
+  }
+  if (lane == 0) {
+    zs[w] = z2;
+    rs[w] = rows;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < N; i += blockDim.x) {
+    float s = 0.f;
+#pragma unroll
+    for (int v = 0; v < kGradWarps; ++v) s += grad_smem[v * S::MAXN + i];
+    part[static_cast<size_t>(blockIdx.x) * N + i] = s;
+    loads[static_cast<size_t>(blockIdx.x) * (N + 1) + i] = hist[i];
+  }
+  if (threadIdx.x == 0) {
+    double s = 0.0;
+    int r = 0;
+    for (int v = 0; v < kGradWarps; ++v) {
+      s += zs[v];
+      r += rs[v];
+    }
+    zpart[blockIdx.x] = s;
+    loads[static_cast<size_t>(blockIdx.x) * (N + 1) + N] = r;
+  }
+}
+
+// Sums of one row, by a warp, for rows of more experts than registers hold.
 struct RowSums {
   float m, z, s;  // largest logit, sum of unit_softmax, sum of unit_sigmoid
 };
-template <typename Tl>
-__device__ __forceinline__ RowSums row_sums(const Tl* row, int N, int lane, bool sigmoid) {
+__device__ __forceinline__ RowSums row_sums(const Logits& x, int t, int N, int lane, bool sigmoid) {
   RowSums r;
   float m = -INFINITY;
-  for (int e = lane; e < N; e += 32) m = fmaxf(m, to_f32(row[e]));
+  for (int e = lane; e < N; e += 32) m = fmaxf(m, x.at(t, e));
   r.m = warp_max(m);
   const float low = fminf(r.m, 0.f);
   float z = 0.f, s = 0.f;
   for (int e = lane; e < N; e += 32) {
-    const float l = to_f32(row[e]);
+    const float l = x.at(t, e);
     if (masked_logit(l)) continue;
     z += unit_softmax(l, r.m);
     if (sigmoid) s += unit_sigmoid(l, low);
@@ -41,171 +196,432 @@ __device__ __forceinline__ RowSums row_sums(const Tl* row, int N, int lane, bool
   return r;
 }
 
-// Per-block sums of the losses' terms: part [grid][N] sums of p_te, zpart
-// [grid] of lse^2, and the counts of chosen slots and of rows into load (zeroed).
-template <typename Tl>
-__global__ __launch_bounds__(kGradWarps * 32) void balance_rows_kernel(const Tl* __restrict__ logits, long long ld,
-                                                                       int T, int N, int k, int score,
+// balance_rows_kernel for such rows: a warp a row, the sums in shared memory.
+__global__ __launch_bounds__(kGradWarps * 32) void balance_long_kernel(const Logits x, int T, int N, int k, int sig,
                                                                        const int32_t* __restrict__ idx,
                                                                        float* __restrict__ part,
                                                                        double* __restrict__ zpart,
-                                                                       int32_t* __restrict__ load) {
-  extern __shared__ float col[];  // [kGradWarps][N]
+                                                                       int32_t* __restrict__ loads) {
+  extern __shared__ __align__(128) float grad_smem[];  // [kGradWarps][N], then the counts [N]
   __shared__ double zs[kGradWarps];
+  __shared__ int rs[kGradWarps];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  float* mine = col + static_cast<size_t>(w) * N;
+  int* hist = reinterpret_cast<int*>(grad_smem + static_cast<size_t>(kGradWarps) * N);
+  float* mine = grad_smem + static_cast<size_t>(w) * N;
   for (int e = lane; e < N; e += 32) mine[e] = 0.f;
-  const bool sig = score == BFMOE_SCORE_SIGMOID;
+  for (int e = threadIdx.x; e < N; e += blockDim.x) hist[e] = 0;
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
   double z2 = 0.0;
   int rows = 0;
   for (int t = blockIdx.x * kGradWarps + w; t < T; t += gridDim.x * kGradWarps) {
-    const Tl* row = logits + static_cast<long long>(t) * ld;
-    const RowSums r = row_sums(row, N, lane, sig);
+    const RowSums r = row_sums(x, t, N, lane, sig != 0);
     if (!(r.m > -INFINITY)) continue;
     const float low = fminf(r.m, 0.f), inv = 1.f / r.s;
     for (int e = lane; e < N; e += 32) {
-      const float l = to_f32(row[e]);
+      const float l = x.at(t, e);
       if (!masked_logit(l)) mine[e] += (sig ? unit_sigmoid(l, low) : unit_softmax(l, r.m)) * inv;
     }
-    const double lse = static_cast<double>(r.m) + static_cast<double>(logf(r.z));
+    const double lse = static_cast<double>(row_lse(r.m, r.z));
     z2 += lse * lse;
     ++rows;
     if (lane < k) {
       const int e = idx[static_cast<long long>(t) * k + lane];
-      if (e >= 0 && e < N) atomicAdd(load + e, 1);
+      if (e >= 0 && e < N) atomicAdd(hist + e, 1);
       else report_error(BFMOE_EDEVICE_BOUNDS, static_cast<unsigned>(t));
     }
   }
   if (lane == 0) {
     zs[w] = z2;
-    if (rows) atomicAdd(load + N, rows);
+    rs[w] = rows;
   }
   __syncthreads();
   for (int e = threadIdx.x; e < N; e += blockDim.x) {
     float s = 0.f;
-    for (int q = 0; q < kGradWarps; ++q) s += col[static_cast<size_t>(q) * N + e];
+    for (int v = 0; v < kGradWarps; ++v) s += grad_smem[static_cast<size_t>(v) * N + e];
     part[static_cast<size_t>(blockIdx.x) * N + e] = s;
+    loads[static_cast<size_t>(blockIdx.x) * (N + 1) + e] = hist[e];
   }
   if (threadIdx.x == 0) {
     double s = 0.0;
-    for (int q = 0; q < kGradWarps; ++q) s += zs[q];
+    int r = 0;
+    for (int v = 0; v < kGradWarps; ++v) {
+      s += zs[v];
+      r += rs[v];
+    }
     zpart[blockIdx.x] = s;
+    loads[static_cast<size_t>(blockIdx.x) * (N + 1) + N] = r;
   }
 }
 
-__global__ __launch_bounds__(1024) void balance_finish_kernel(const float* __restrict__ part,
-                                                              const double* __restrict__ zpart, int blocks, int N,
-                                                              int k, const int32_t* __restrict__ load,
-                                                              float* __restrict__ loss) {
-  __shared__ double red[32];
-  double s = 0.0;
-  for (int e = threadIdx.x; e < N; e += blockDim.x) {
-    double p = 0.0;
-    for (int b = 0; b < blocks; ++b) p += static_cast<double>(part[static_cast<size_t>(b) * N + e]);
-    s += p * static_cast<double>(load[e]);
-  }
-  s = warp_sum(s);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+// The blocks' sums added up, by one cluster; each of its blocks takes a share
+// of the experts, its threads slices of the rows of part and loads.
+constexpr int kFinishBlocks = 8;
+constexpr int kFinishThreads = 1024;
+__global__ __cluster_dims__(kFinishBlocks, 1, 1) __launch_bounds__(kFinishThreads) void balance_finish_kernel(
+    const float* __restrict__ part, const double* __restrict__ zpart, const int32_t* __restrict__ loads, int blocks,
+    int N, int k, int32_t* __restrict__ load, float* __restrict__ loss) {
+  __shared__ double ps[kFinishThreads];
+  __shared__ int ls[kFinishThreads];
+  __shared__ double share[kFinishBlocks];  // of block 0: each block's sum of load P
+  const int rank = blockIdx.x, tid = threadIdx.x;
+  const int per = (N + kFinishBlocks - 1) / kFinishBlocks;  // <= 512
+  int width = 1;
+  while (width < per) width <<= 1;
+  const int slices = kFinishThreads / width, e = rank * per + (tid & (width - 1)), slice = tid / width;
+  const bool real = (tid & (width - 1)) < per && e < N;
+  pdl_wait();
+  pdl_trigger();
+  double p = 0.0;
+  int c = 0;
+  if (real)
+    for (int b = slice; b < blocks; b += slices) {
+      p += static_cast<double>(part[static_cast<size_t>(b) * N + e]);
+      c += loads[static_cast<size_t>(b) * (N + 1) + e];
+    }
+  ps[tid] = p;
+  ls[tid] = c;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    double b = 0.0, z = 0.0;
-    for (int q = 0; q < static_cast<int>(blockDim.x) / 32; ++q) b += red[q];
-    for (int q = 0; q < blocks; ++q) z += zpart[q];
-    const double R = static_cast<double>(load[N]);
-    loss[0] = R > 0.0 ? static_cast<float>(b * N / (static_cast<double>(k) * R * R)) : 0.f;
-    loss[1] = R > 0.0 ? static_cast<float>(z / R) : 0.f;
+  for (int s = kFinishThreads / 2; s >= width; s >>= 1) {
+    if (tid < s) {
+      ps[tid] += ps[tid + s];
+      ls[tid] += ls[tid + s];
+    }
+    __syncthreads();
   }
-}
-
-template <typename Tl>
-__global__ __launch_bounds__(kGradWarps * 32) void route_backward_kernel(
-    const Tl* logits, long long ld, int T, int N, int k, RouteCfg cfg, const int32_t* __restrict__ idx,
-    const float* __restrict__ dgates, const int32_t* __restrict__ load, const float* __restrict__ dloss, Tl* dlogits,
-    long long ldd) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const bool sig = cfg.score == BFMOE_SCORE_SIGMOID;
-  const bool dense = dgates && !sig && !cfg.renorm;  // every logit moves every gate
-  float cb = 0.f, cz = 0.f, fs = 0.f;
-  if (load) {
-    const float R = static_cast<float>(load[N]);
-    if (R > 0.f) {
-      cb = dloss[0] * static_cast<float>(N) / R;
-      cz = 2.f * dloss[1] / R;
-      fs = 1.f / (static_cast<float>(k) * R);
+  double mine = 0.0;
+  if (tid < width && real) {
+    load[e] = ls[tid];
+    mine = ps[tid] * static_cast<double>(ls[tid]);
+  }
+  __syncthreads();
+  ps[tid] = mine;
+  __syncthreads();
+  for (int s = kFinishThreads / 2; s > 0; s >>= 1) {
+    if (tid < s) ps[tid] += ps[tid + s];
+    __syncthreads();
+  }
+  if (tid == 0) {
+    uint32_t there;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(there) : "r"(smem_u32(share + rank)));
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(there), "d"(ps[0]) : "memory");
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (rank == 0) {
+    // rows and z, a warp each
+    double z = 0.0;
+    int r = 0;
+    if (tid < 32)
+      for (int b = tid; b < blocks; b += 32) {
+        z += zpart[b];
+        r += loads[static_cast<size_t>(b) * (N + 1) + N];
+      }
+    if (tid < 32) {
+      z = warp_sum(z);
+      r = __reduce_add_sync(FULL_MASK, r);
+      if (tid == 0) {
+        double b = 0.0;
+        for (int q = 0; q < kFinishBlocks; ++q) b += share[q];
+        const double R = static_cast<double>(r);
+        load[N] = r;
+        loss[0] = r > 0 ? static_cast<float>(b * N / (static_cast<double>(k) * R * R)) : 0.f;
+        loss[1] = r > 0 ? static_cast<float>(z / R) : 0.f;
+      }
     }
   }
+}
+
+struct RouteGrad {
+  const int32_t* idx;
+  const float* dgates;   // or NULL
+  const int32_t* load;   // or NULL
+  const float* dloss;
+  void* out;
+  long long ld_out;
+  int wide_out;
+};
+
+// Factors of the losses: balance times N / R and 1 / (k R), z times 2 / R.
+struct LossFactors {
+  float cb, cz;
+  __device__ __forceinline__ LossFactors(const RouteGrad& g, int N, int k) {
+    cb = cz = 0.f;
+    if (g.load) {
+      const float R = static_cast<float>(g.load[N]);
+      if (R > 0.f) {
+        cb = g.dloss[0] * static_cast<float>(N) / R / (static_cast<float>(k) * R);
+        cz = 2.f * g.dloss[1] / R;
+      }
+    }
+  }
+};
+
+// A row in registers: the gradient of every logit is p_e (a_e + K) from the
+// losses and the plain softmax's gates (a_e = cb load_e, K the row's sums), and
+// each chosen expert has its own term, which reaches its lane through shared
+// memory.  Where only chosen experts have one, the row is not read.
+template <class S, bool SIGMOID>
+__global__ __launch_bounds__(kGradWarps * 32, kGradRowBlocks<S>) void route_backward_kernel(const Logits x, int T, int N,
+                                                                                            int k, const RouteCfg cfg,
+                                                                                            const RouteGrad g) {
+  constexpr int LPR = S::LPR, V = S::V;
+  extern __shared__ __align__(128) float grad_smem[];  // a [MAXN], the rows' chosen terms [warps * ROWS][MAXN], buffers
+  __shared__ uint64_t full_s[kGradWarps * 2];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, q = lane & (LPR - 1);
+  float* mine = grad_smem + S::MAXN + (w * S::ROWS + lane / LPR) * S::MAXN;
+#pragma unroll
+  for (int i = 0; i < V; ++i) mine[i * LPR + q] = 0.f;
+  pdl_wait();
+  pdl_trigger();
+  const LossFactors f(g, N, k);
+  for (int e = threadIdx.x; e < S::MAXN; e += blockDim.x)
+    grad_smem[e] = e < N && f.cb != 0.f ? f.cb * static_cast<float>(g.load[e]) : 0.f;
+  __syncthreads();
+  const bool dense = g.dgates && !SIGMOID && !cfg.renorm;  // every logit moves every gate
+  const bool need_row = dense || f.cb != 0.f || f.cz != 0.f;
+  const int step = gridDim.x * kGradWarps * S::ROWS;
+  int t0 = (blockIdx.x * kGradWarps + w) * S::ROWS;
+  RowFeed<S> feed;
+  if (need_row)
+    feed.start(x, t0, T, N, lane,
+               reinterpret_cast<uint8_t*>(grad_smem + S::MAXN * (1 + kGradWarps * S::ROWS)) +
+                   static_cast<size_t>(w) * RowFeed<S>::BUFFER,
+               full_s + w * 2);
+  else
+    feed.here = nullptr;
+  int e_next = -1;
+  float dg_next = 0.f;
+  auto slot = [&](int t) {
+    e_next = -1;
+    dg_next = 0.f;
+    if (g.dgates && q < k && t < T) {
+      e_next = g.idx[static_cast<long long>(t) * k + q];
+      dg_next = g.dgates[static_cast<long long>(t) * k + q] * cfg.scale;
+    }
+  };
+  slot(t0 + lane / LPR);
+  for (; t0 < T; t0 += step) {
+    const int t = min(t0 + lane / LPR, T - 1);
+    const bool has = t0 + lane / LPR < T;
+    float l[V], u[V], tt[V], a[V];
+    if (need_row && !feed.take(x, t0, step, T, N, lane, l)) return;
+    int e = e_next;
+    const float dg = dg_next;
+    slot(t0 + step + lane / LPR);
+    // the chosen: lane q < k holds slot q
+    float le = -INFINITY;
+    bool live = false;
+    if (g.dgates) {
+      if (q < k && has && (e < 0 || e >= N)) {
+        report_error(BFMOE_EDEVICE_BOUNDS, static_cast<unsigned>(t));
+        e = -1;
+      }
+      if (e >= 0) le = feed.at(x, t, e);
+      live = e >= 0 && !masked_logit(le);
+    }
+    float m = 0.f, inv = 0.f, pa = 0.f, lse = 0.f;
+    if (need_row) {
+      m = row_max<S>(l);
+      load_cells<S>(grad_smem, q, a);
+      float s = 0.f;
+      if constexpr (SIGMOID) {
+        if (f.cz != 0.f) {  // softmax_e lse cz is added at the end
+          const float z = row_softmax<S>(l, m, u);
+          lse = m > -INFINITY ? row_lse(m, z) * f.cz * rcp_fast(z) : 0.f;
+        }
+        row_sigmoid<S>(l, m, u, tt);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s += u[i];
+        s = seg_sum<LPR>(s);
+      } else {
+        s = row_softmax<S>(l, m, u);
+        lse = m > -INFINITY ? row_lse(m, s) * f.cz : 0.f;
+      }
+      inv = s > 0.f ? rcp_fast(s) : 0.f;
+      if (f.cb != 0.f) {
+        float b = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) b = fmaf(u[i], a[i], b);
+        pa = seg_sum<LPR>(b) * inv;
+      }
+    }
+    float d = 0.f, dot = 0.f;
+    if (g.dgates) {
+      if (dense) {
+        d = live ? unit_softmax(le, m) * inv * dg : 0.f;
+        dot = seg_sum<LPR>(d);
+      } else if (cfg.renorm) {
+        const float top = seg_max<LPR>(live ? le : -INFINITY);
+        const float v = !live ? 0.f : (SIGMOID ? unit_sigmoid(le, fminf(top, 0.f)) : unit_softmax(le, top));
+        const float s = seg_sum<LPR>(v);
+        const float r = s > 0.f ? v * rcp_fast(s) : 0.f;
+        d = r * (dg - seg_sum<LPR>(r * dg));
+      } else {
+        d = live ? dg * sigmoid_fast(le) : 0.f;
+      }
+      if (SIGMOID) d = live ? d * sigmoid_fast(-le) : 0.f;
+      // the terms of one expert chosen twice add up in slot order
+      const unsigned same = __match_any_sync(FULL_MASK, e >= 0 ? (lane & ~(LPR - 1)) * BFMOE_MAX_EXPERTS + e : ~lane);
+      if (__any_sync(FULL_MASK, (same & (same - 1)) != 0u)) {
+        float all = 0.f;
+        for (int o = 0; o < k; ++o) {
+          const float v = __shfl_sync(FULL_MASK, d, o, LPR);
+          if ((same >> ((lane & ~(LPR - 1)) + o)) & 1u) all += v;
+        }
+        d = all;
+      }
+      if (e >= 0) mine[e] = d;
+      __syncwarp();
+    }
+    float o[V];
+    if (g.dgates) {
+      load_cells<S>(mine, q, o);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] = 0.f;
+    }
+    if (need_row) {
+      if constexpr (SIGMOID) {
+        if (f.cb != 0.f) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) o[i] = fmaf(u[i] * inv * tt[i], a[i] - pa, o[i]);
+        }
+        if (f.cz != 0.f) {
+          row_softmax<S>(l, m, u);
+#pragma unroll
+          for (int i = 0; i < V; ++i) o[i] = fmaf(u[i], lse, o[i]);
+        }
+      } else {
+        const float K = lse - pa - dot;
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = fmaf(u[i] * inv, a[i] + K, o[i]);
+      }
+    }
+    if (has) {
+      const long long at = static_cast<long long>(t) * g.ld_out;
+#pragma unroll
+      for (int c = 0; c < S::C; ++c) {
+        const int e0 = (c * LPR + q) * S::CE;
+        const float* v = o + c * S::CE;
+        if (g.wide_out) {
+          if (e0 < N) {
+            if (x.bf16) {
+              uint32_t b[S::CE / 2];
+#pragma unroll
+              for (int h = 0; h < S::CE / 2; ++h) {
+                const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * h], v[2 * h + 1]);
+                b[h] = *reinterpret_cast<const uint32_t*>(&p);
+              }
+              auto* p = static_cast<__nv_bfloat16*>(g.out) + at + e0;
+              if constexpr (S::CE == 8) *reinterpret_cast<uint4*>(p) = make_uint4(b[0], b[1], b[2], b[3]);
+              else *reinterpret_cast<uint2*>(p) = make_uint2(b[0], b[1]);
+            } else {
+#pragma unroll
+              for (int h = 0; h < S::CE; h += 4)
+                *reinterpret_cast<float4*>(static_cast<float*>(g.out) + at + e0 + h) =
+                    make_float4(v[h], v[h + 1], v[h + 2], v[h + 3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < S::CE; ++i)
+            if (e0 + i < N) {
+              if (x.bf16) static_cast<__nv_bfloat16*>(g.out)[at + e0 + i] = __float2bfloat16_rn(v[i]);
+              else static_cast<float*>(g.out)[at + e0 + i] = v[i];
+            }
+        }
+      }
+    }
+    if (g.dgates) {  // every lane has read its cells
+      __syncwarp();
+      if (e >= 0) mine[e] = 0.f;
+      __syncwarp();
+    }
+  }
+}
+
+// Rows of more experts than registers hold: a warp a row, several passes.
+__global__ __launch_bounds__(kGradWarps * 32) void route_backward_long_kernel(const Logits x, int T, int N, int k,
+                                                                              const RouteCfg cfg, const RouteGrad g) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  pdl_wait();
+  pdl_trigger();
+  const bool sig = cfg.score == BFMOE_SCORE_SIGMOID;
+  const bool dense = g.dgates && !sig && !cfg.renorm;
+  const LossFactors f(g, N, k);
   for (int t = blockIdx.x * kGradWarps + w; t < T; t += gridDim.x * kGradWarps) {
-    const Tl* row = logits + static_cast<long long>(t) * ld;
-    Tl* out = dlogits + static_cast<long long>(t) * ldd;
     RowSums r{-INFINITY, 0.f, 0.f};
-    if (load || dense) r = row_sums(row, N, lane, sig);
+    if (g.load || dense) r = row_sums(x, t, N, lane, sig);
     const float low = fminf(r.m, 0.f);
     const float inv_z = r.z > 0.f ? 1.f / r.z : 0.f, inv_s = r.s > 0.f ? 1.f / r.s : 0.f;
-    // the chosen: lane j < k holds slot j and its share of the gradient
     int e = -1;
-    float d = 0.f, dense_sum = 0.f;
-    if (dgates) {
+    float d = 0.f, dot = 0.f;
+    if (g.dgates) {
       float l = -INFINITY, dg = 0.f;
       if (lane < k) {
-        e = idx[static_cast<long long>(t) * k + lane];
+        e = g.idx[static_cast<long long>(t) * k + lane];
         if (e < 0 || e >= N) {
           report_error(BFMOE_EDEVICE_BOUNDS, static_cast<unsigned>(t));
           e = -1;
         } else {
-          l = to_f32(row[e]);
-          dg = dgates[static_cast<long long>(t) * k + lane] * cfg.scale;
+          l = x.at(t, e);
+          dg = g.dgates[static_cast<long long>(t) * k + lane] * cfg.scale;
         }
       }
       const bool live = e >= 0 && !masked_logit(l);
       if (dense) {
         d = live ? unit_softmax(l, r.m) * inv_z * dg : 0.f;
-        dense_sum = warp_sum(d);
+        dot = warp_sum(d);
       } else if (cfg.renorm) {
         const float m = warp_max(live ? l : -INFINITY);
         const float u = !live ? 0.f : (sig ? unit_sigmoid(l, fminf(m, 0.f)) : unit_softmax(l, m));
         const float s = warp_sum(u);
         const float q = s > 0.f ? u / s : 0.f;
-        const float dot = warp_sum(q * dg);
-        d = q * (dg - dot);
+        d = q * (dg - warp_sum(q * dg));
       } else {
         d = live ? dg * sigmoid_fast(l) : 0.f;
       }
       if (sig) d = live ? d * sigmoid_fast(-l) : 0.f;
     }
-    float fp = 0.f;
-    if (load && cb != 0.f) {
+    float pa = 0.f;
+    if (f.cb != 0.f) {
       for (int q = lane; q < N; q += 32) {
-        const float l = to_f32(row[q]);
+        const float l = x.at(t, q);
         if (masked_logit(l)) continue;
-        fp += (sig ? unit_sigmoid(l, low) : unit_softmax(l, r.m)) * inv_s * (static_cast<float>(load[q]) * fs);
+        pa += (sig ? unit_sigmoid(l, low) : unit_softmax(l, r.m)) * inv_s * (f.cb * static_cast<float>(g.load[q]));
       }
-      fp = warp_sum(fp);
+      pa = warp_sum(pa);
     }
-    const float lse = r.m + logf(r.z);
+    const float lse = f.cz != 0.f ? f.cz * row_lse(r.m, r.z) : 0.f;
     __syncwarp();
     for (int q0 = 0; q0 < N; q0 += 32) {
       const int q = q0 + lane;
-      float g = 0.f;
+      float o = 0.f;
       if (q < N) {
-        const float l = to_f32(row[q]);
+        const float l = x.at(t, q);
         if (!masked_logit(l)) {
-          const float p = load || dense ? unit_softmax(l, r.m) * inv_z : 0.f;
-          if (dense) g -= p * dense_sum;
-          if (cb != 0.f) {
+          const float p = dense || f.cb != 0.f || f.cz != 0.f ? unit_softmax(l, r.m) * inv_z : 0.f;
+          if (dense) o -= p * dot;
+          if (f.cb != 0.f) {
             const float ps = sig ? unit_sigmoid(l, low) * inv_s : p;
-            float b = cb * ps * (static_cast<float>(load[q]) * fs - fp);
+            float b = ps * (f.cb * static_cast<float>(g.load[q]) - pa);
             if (sig) b *= sigmoid_fast(-l);
-            g += b;
+            o += b;
           }
-          if (cz != 0.f) g += cz * lse * p;
+          o += lse * p;
         }
       }
       for (int j = 0; j < k; ++j) {
         const int ej = __shfl_sync(FULL_MASK, e, j);
         const float dj = __shfl_sync(FULL_MASK, d, j);
-        if (ej == q) g += dj;
+        if (ej == q) o += dj;
       }
-      if (q < N) out[q] = from_f32<Tl>(g);
+      if (q < N) {
+        const long long at = static_cast<long long>(t) * g.ld_out + q;
+        if (x.bf16) static_cast<__nv_bfloat16*>(g.out)[at] = __float2bfloat16_rn(o);
+        else static_cast<float*>(g.out)[at] = o;
+      }
     }
     __syncwarp();
   }
