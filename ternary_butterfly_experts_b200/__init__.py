@@ -31,19 +31,31 @@ __all__ = [
 ]
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(stream=None):
+    """The stream's handle as an integer.  torch.cuda.current_stream() builds an
+    object (3 us); the handle alone is there for generated kernels."""
+    if stream is not None:
+        return stream.cuda_stream
     torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None:
+        return raw(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need(t, name, dtype=None, cuda=True, contiguous=True):
@@ -406,6 +418,7 @@ class Scoring:
         self.renormalize, self.scale = bool(renormalize), float(scale)
         self.c = capi.BfmoeScoring(self.SCORES[score], n_groups, top_groups, self.GROUP_SCORES[group_score],
                                    int(self.renormalize), self.scale)
+        self.ref = ctypes.byref(self.c)
 
     def __repr__(self):
         return (f"Scoring(score={self.score!r}, n_groups={self.n_groups}, top_groups={self.top_groups}, "
@@ -413,24 +426,22 @@ class Scoring:
 
 
 def _here(stream, *named):
-    """The stream handle of a call whose tensors (name, tensor or None) must
-    all live on the current CUDA device."""
-    torch = _torch()
-    for name, t in named:
-        if t is not None and not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-    dev = torch.cuda.current_device()
-    for name, t in named:
-        if t is not None and t.device.index != dev:
+    """The stream handle of a call whose tensors (name, tensor or None, ...)
+    must all live on the current CUDA device."""
+    dev = _torch().cuda.current_device()
+    for i in range(1, len(named), 2):
+        t = named[i]
+        if t is not None and t.get_device() != dev:
+            name = named[i - 1]
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
             raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
     return _stream(stream)
 
 
-def _need_shape(t, name, dtype, shape):
-    if t is None:
-        return
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+def _need_shape(t, name, dtype, *shape):
+    if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, got {t.dtype} "
                          f"{tuple(t.shape)}")
 
 
@@ -439,15 +450,19 @@ def _logits(t, name="logits"):
     if t.dim() != 2:
         raise ValueError(f"{name} must be [T][N]")
     T, N = t.shape
-    if N > 1 and t.stride(1) != 1:
+    ld, one = t.stride()
+    if N > 1 and one != 1:
         raise ValueError(f"{name} must have consecutive elements in a row")
-    ld = t.stride(0) if T > 1 else N
-    if ld < N:
+    if T <= 1:
+        ld = N
+    elif ld < N:
         raise ValueError(f"the rows of {name} overlap (stride {ld} for {N} experts)")
     torch = _torch()
-    if t.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    return (BFMOE_BF16 if t.dtype == torch.bfloat16 else BFMOE_F32), T, N, ld
+    if t.dtype is torch.float32:
+        return BFMOE_F32, T, N, ld
+    if t.dtype is torch.bfloat16:
+        return BFMOE_BF16, T, N, ld
+    raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
 
 
 def bfmoe_route_workspace_size(n_experts: int, T: int, k: int) -> int:
@@ -470,12 +485,12 @@ def bfmoe_router_logits(x, w_gate, bias=None, logits=None, ws=None, stream=None)
         raise ValueError("x must be [T][d] and w_gate [N][d]")
     T, d = x.shape
     N = w_gate.shape[0]
-    _need_shape(bias, "bias", torch.float32, (N,))
+    _need_shape(bias, "bias", torch.float32, N)
     code = _dtype_code(x)
     if logits is None:
         logits = torch.empty((T, N), dtype=torch.float32, device=x.device)
-    _need_shape(logits, "logits", torch.float32, (T, N))
-    s = _here(stream, ("x", x), ("w_gate", w_gate), ("bias", bias), ("logits", logits), ("ws", ws))
+    _need_shape(logits, "logits", torch.float32, T, N)
+    s = _here(stream, "x", x, "w_gate", w_gate, "bias", bias, "logits", logits, "ws", ws)
     if ws is None:
         ws = workspace(d, N, T, 1, code, x.device)
     capi.check(capi.lib().bfmoe_router_logits(_ptr(x), code, T, d, _ptr(w_gate), _ptr(bias), N, _ptr(logits),
@@ -491,26 +506,27 @@ def bfmoe_route(logits, k: int, scoring: Scoring, balance_bias=None, ws=None, ou
     and are not built."""
     torch = _torch()
     code, T, N, ld = _logits(logits)
-    _need_shape(balance_bias, "balance_bias", torch.float32, (N,))
-    dev = logits.device
+    _need_shape(balance_bias, "balance_bias", torch.float32, N)
     if out is None:
-        i32 = dict(dtype=torch.int32, device=dev)
-        out = (torch.empty((T, k), **i32), torch.empty((T, k), dtype=torch.float32, device=dev))
-        out += (torch.empty((N,), **i32), torch.empty((N + 1,), **i32),
-                torch.empty((T * k,), **i32)) if buckets else (None, None, None)
+        new, i32 = logits.new_empty, torch.int32
+        out = (new((T, k), dtype=i32), new((T, k), dtype=torch.float32))
+        out += (new(N, dtype=i32), new(N + 1, dtype=i32), new(T * k, dtype=i32)) if buckets else (None, None, None)
+        idx, gates, counts, offsets, rows = out
+        s = _here(stream, "logits", logits, "balance_bias", balance_bias, "ws", ws)
     else:
-        _need_shape(out[0], "idx", torch.int32, (T, k))
-        _need_shape(out[1], "gates", torch.float32, (T, k))
-        for t, name, shape in ((out[2], "counts", (N,)), (out[3], "offsets", (N + 1,)), (out[4], "rows", (T * k,))):
-            _need_shape(t, name, torch.int32, shape)
-    idx, gates, counts, offsets, rows = out
-    s = _here(stream, ("logits", logits), ("balance_bias", balance_bias), ("idx", idx), ("gates", gates),
-              ("counts", counts), ("offsets", offsets), ("rows", rows), ("ws", ws))
-    if counts is not None:
-        ws = _route_ws(ws, N, T, k, dev)
+        idx, gates, counts, offsets, rows = out
+        _need_shape(idx, "idx", torch.int32, T, k)
+        _need_shape(gates, "gates", torch.float32, T, k)
+        _need_shape(counts, "counts", torch.int32, N)
+        _need_shape(offsets, "offsets", torch.int32, N + 1)
+        _need_shape(rows, "rows", torch.int32, T * k)
+        s = _here(stream, "logits", logits, "balance_bias", balance_bias, "idx", idx, "gates", gates,
+                  "counts", counts, "offsets", offsets, "rows", rows, "ws", ws)
+    if counts is not None and ws is None:
+        ws = _route_ws(ws, N, T, k, logits.device)
     capi.check(capi.lib().bfmoe_route(
-        _ptr(logits), code, T, ld, N, k, ctypes.byref(scoring.c), _ptr(balance_bias), _ptr(idx), _ptr(gates),
-        _ptr(counts), _ptr(offsets), _ptr(rows), _ptr(ws), ws.numel() if ws is not None else 0, s))
+        logits.data_ptr(), code, T, ld, N, k, scoring.ref, _ptr(balance_bias), _ptr(idx), _ptr(gates),
+        _ptr(counts), _ptr(offsets), _ptr(rows), _ptr(ws), ws.nbytes if ws is not None else 0, s))
     return out
 
 
@@ -525,17 +541,17 @@ def bfmoe_balance_loss(logits, idx, score: str = "softmax", ws=None, out=None, s
     if idx.dim() != 2:
         raise ValueError("idx must be [T][k]")
     k = idx.shape[1]
-    _need_shape(idx, "idx", torch.int32, (T, k))
+    _need_shape(idx, "idx", torch.int32, T, k)
     if out is None:
-        out = (torch.empty((2,), dtype=torch.float32, device=logits.device),
-               torch.empty((N + 1,), dtype=torch.int32, device=logits.device))
+        out = (logits.new_empty(2, dtype=torch.float32), logits.new_empty(N + 1, dtype=torch.int32))
     loss, load = out
-    _need_shape(loss, "loss", torch.float32, (2,))
-    _need_shape(load, "load", torch.int32, (N + 1,))
-    s = _here(stream, ("logits", logits), ("idx", idx), ("loss", loss), ("load", load), ("ws", ws))
-    ws = _route_ws(ws, N, T, k, logits.device)
-    capi.check(capi.lib().bfmoe_balance_loss(_ptr(logits), code, T, ld, N, k, Scoring.SCORES[score], _ptr(idx),
-                                             _ptr(loss), _ptr(load), _ptr(ws), ws.numel(), s))
+    _need_shape(loss, "loss", torch.float32, 2)
+    _need_shape(load, "load", torch.int32, N + 1)
+    s = _here(stream, "logits", logits, "idx", idx, "loss", loss, "load", load, "ws", ws)
+    if ws is None:
+        ws = _route_ws(ws, N, T, k, logits.device)
+    capi.check(capi.lib().bfmoe_balance_loss(logits.data_ptr(), code, T, ld, N, k, Scoring.SCORES[score], _ptr(idx),
+                                             loss.data_ptr(), load.data_ptr(), ws.data_ptr(), ws.nbytes, s))
     return out
 
 
@@ -549,20 +565,20 @@ def bfmoe_route_backward(logits, idx, scoring: Scoring, dgates=None, load=None, 
     if idx.dim() != 2:
         raise ValueError("idx must be [T][k]")
     k = idx.shape[1]
-    _need_shape(idx, "idx", torch.int32, (T, k))
-    _need_shape(dgates, "dgates", torch.float32, (T, k))
-    _need_shape(load, "load", torch.int32, (N + 1,))
-    _need_shape(dloss, "dloss", torch.float32, (2,))
+    _need_shape(idx, "idx", torch.int32, T, k)
+    _need_shape(dgates, "dgates", torch.float32, T, k)
+    _need_shape(load, "load", torch.int32, N + 1)
+    _need_shape(dloss, "dloss", torch.float32, 2)
     if dlogits is None:
-        dlogits = torch.empty((T, N), dtype=logits.dtype, device=logits.device)
-    if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape:
-        raise ValueError("dlogits must match logits in shape and dtype")
-    ldd = _logits(dlogits, "dlogits")[3]
-    s = _here(stream, ("logits", logits), ("idx", idx), ("dgates", dgates), ("load", load), ("dloss", dloss),
-              ("dlogits", dlogits))
+        dlogits, ldd = logits.new_empty((T, N)), N
+    else:
+        if dlogits.dtype is not logits.dtype or dlogits.shape != logits.shape:
+            raise ValueError("dlogits must match logits in shape and dtype")
+        ldd = _logits(dlogits, "dlogits")[3]
+    s = _here(stream, "logits", logits, "idx", idx, "dgates", dgates, "load", load, "dloss", dloss, "dlogits", dlogits)
     capi.check(capi.lib().bfmoe_route_backward(
-        _ptr(logits), code, T, ld, N, k, ctypes.byref(scoring.c), _ptr(idx), _ptr(dgates), _ptr(load), _ptr(dloss),
-        _ptr(dlogits), ldd, s))
+        logits.data_ptr(), code, T, ld, N, k, scoring.ref, _ptr(idx), _ptr(dgates), _ptr(load), _ptr(dloss),
+        dlogits.data_ptr(), ldd, s))
     return dlogits
 
 
@@ -577,15 +593,15 @@ def bfmoe_expert_backward(layer: "Layer", x, k: int, routing, gy, ws=None, strea
     if d != layer.d:
         raise ValueError(f"x has width {d}, layer has d={layer.d}")
     idx, gates, _counts, offsets, rows = routing
-    _need_shape(gy, "gy", torch.float32, (T, d))
-    _need_shape(idx, "idx", torch.int32, (T, k))
-    _need_shape(gates, "gates", torch.float32, (T, k))
+    _need_shape(gy, "gy", torch.float32, T, d)
+    _need_shape(idx, "idx", torch.int32, T, k)
+    _need_shape(gates, "gates", torch.float32, T, k)
     for t, name, n in ((offsets, "offsets", N + 1), (rows, "rows", T * k)):
         if t is None:
             raise ValueError(f"{name} is required")
-        _need_shape(t, name, torch.int32, (n,))
-    s = _here(stream, ("x", x), ("gy", gy), ("idx", idx), ("gates", gates), ("offsets", offsets), ("rows", rows),
-              ("theta", layer.theta), ("ws", ws))
+        _need_shape(t, name, torch.int32, n)
+    s = _here(stream, "x", x, "gy", gy, "idx", idx, "gates", gates, "offsets", offsets, "rows", rows,
+              "theta", layer.theta, "ws", ws)
     if ws is None:
         ws = torch.empty(max(bfmoe_backward_workspace_size(d, N, T, k), 256), dtype=torch.uint8, device=x.device)
     f = dict(dtype=torch.float32, device=x.device)
@@ -638,23 +654,21 @@ class GradList:
         self.ws = torch.empty(bfmoe_grad_workspace_size(), dtype=torch.uint8, device=dev)
 
 
-def _grad_list(grads):
+def _grad_call(grads, norm, stream):
+    """(GradList, norm, stream handle) of a call on the current device."""
+    torch = _torch()
     g = grads if isinstance(grads, GradList) else GradList(grads)
-    dev = _torch().cuda.current_device()
-    if g.device.index != dev:
-        raise ValueError(f"the gradients are on {g.device}, the current device is cuda:{dev}")
-    return g
+    if norm is None:
+        norm = g.ws.new_empty(1, dtype=torch.float32)
+    else:
+        _need_shape(norm, "norm", torch.float32, 1)
+    return g, norm, _here(stream, "the gradients", g.ws, "norm", norm)
 
 
 def bfmoe_grad_norm(grads, norm=None, stream=None):
     """The global norm (float32 [1]) of a GradList or of a sequence of tensors."""
-    torch = _torch()
-    g = _grad_list(grads)
-    if norm is None:
-        norm = torch.empty((1,), dtype=torch.float32, device=g.device)
-    _need_shape(norm, "norm", torch.float32, (1,))
-    s = _here(stream, ("norm", norm))
-    capi.check(capi.lib().bfmoe_grad_norm(g.c, g.n, _ptr(norm), _ptr(g.ws), g.ws.numel(), s))
+    g, norm, s = _grad_call(grads, norm, stream)
+    capi.check(capi.lib().bfmoe_grad_norm(g.c, g.n, norm.data_ptr(), g.ws.data_ptr(), g.ws.nbytes, s))
     return norm
 
 
@@ -662,13 +676,8 @@ def bfmoe_grad_clip(grads, max_norm: float, norm=None, stream=None):
     """Scale a GradList (or a sequence of tensors, in place) by
     min(1, max_norm / norm); returns the norm before it (float32 [1]).  A norm
     that is not finite leaves the gradients as they are."""
-    torch = _torch()
-    g = _grad_list(grads)
-    if norm is None:
-        norm = torch.empty((1,), dtype=torch.float32, device=g.device)
-    _need_shape(norm, "norm", torch.float32, (1,))
-    s = _here(stream, ("norm", norm))
-    capi.check(capi.lib().bfmoe_grad_clip(g.c, g.n, max_norm, _ptr(norm), _ptr(g.ws), g.ws.numel(), s))
+    g, norm, s = _grad_call(grads, norm, stream)
+    capi.check(capi.lib().bfmoe_grad_clip(g.c, g.n, max_norm, norm.data_ptr(), g.ws.data_ptr(), g.ws.nbytes, s))
     return norm
 
 

@@ -833,6 +833,40 @@ cudaError_t build_buckets(const int32_t* idx, long long R, int k, int N, bool ha
     attr_set(done);
   }
   cudaError_t e = cudaSuccess;
+  if (!have_histograms && !pad_out && R <= kBucketClusterRows && N <= kBucketClusterExperts) {
+    // one launch where it fits (and where 16 SMs can hold a cluster)
+    static std::atomic<uint64_t> ready{0};
+    static std::atomic<uint64_t> fits{0};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kBucketCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = kBucketCluster;
+    cfg.blockDim = 1024;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (needs_attr(ready)) {
+      int clusters = 0;
+      cfg.dynamicSmemBytes = bucket_cluster_smem(kBucketClusterExperts);
+      if (cudaFuncSetAttribute(bucket_cluster_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+          cudaFuncSetAttribute(bucket_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(cfg.dynamicSmemBytes)) == cudaSuccess &&
+          cudaOccupancyMaxActiveClusters(&clusters, bucket_cluster_kernel, &cfg) == cudaSuccess && clusters > 0)
+        attr_set(fits);
+      cudaGetLastError();
+      attr_set(ready);
+    }
+    if (!needs_attr(fits)) {
+      cfg.dynamicSmemBytes = bucket_cluster_smem(N);
+      return launch("bucket_build", s, [&] {
+        cudaLaunchKernelEx(&cfg, bucket_cluster_kernel, idx, R, N, counts, offsets, rows);
+      });
+    }
+  }
   if (!have_histograms) {
     e = launch("bucket_count", s, [&] { bucket_count_kernel<<<nchunks, chunk, N * 4, s>>>(idx, R, N, cc); });
     if (e != cudaSuccess) return e;

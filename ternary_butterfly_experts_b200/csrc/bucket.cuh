@@ -240,4 +240,107 @@ __global__ __launch_bounds__(256) void bucket_pad_kernel(const int32_t* __restri
   }
 }
 
+// The whole bucket build in one launch for up to kBucketClusterRows rows of up
+// to kBucketClusterExperts experts: one cluster of 16 CTAs, a warp taking a run
+// of consecutive rows (at most 2 steps of 32).
+//   1  rows of each expert in each warp's run (leaders of equal experts add)
+//   2  prefix over the CTA's warps; the CTAs' totals read through distributed
+//      shared memory: prefix over CTAs, counts, offsets
+//   3  position = offset + CTAs before + warps before + rank in the warp
+// Launches bound small batches: count, scan and scatter are three.  (With 8
+// steps it took 20 us for 131072 rows, the three launches together 7.)
+constexpr int kBucketCluster = 16;
+constexpr int kBucketClusterSteps = 2;
+constexpr long long kBucketClusterRows = kBucketCluster * 32LL * 32 * kBucketClusterSteps;
+constexpr int kBucketClusterExperts = 2048;
+__host__ __device__ constexpr size_t bucket_cluster_smem(int N) {
+  return static_cast<size_t>(N) * 64 + static_cast<size_t>(3 * N + 4) * 4;
+}
+
+__global__ __launch_bounds__(1024) void bucket_cluster_kernel(const int32_t* __restrict__ idx, long long R, int N,
+                                                              int32_t* __restrict__ counts_out,
+                                                              int32_t* __restrict__ offsets_out,
+                                                              int32_t* __restrict__ rows) {
+  extern __shared__ __align__(16) uint8_t cluster_smem[];
+  int* tot = reinterpret_cast<int*>(cluster_smem);           // [N] rows of the CTA, then of all
+  int* base = tot + N;                                       // [N]
+  int* off = base + N;                                       // [N + 1]
+  uint16_t* wcnt = reinterpret_cast<uint16_t*>(tot + 3 * N + 4);  // [32][N]
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int rank = blockIdx.x;
+  for (int q = tid; q < N * 16; q += 1024) reinterpret_cast<uint32_t*>(wcnt)[q] = 0u;
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  const int run = static_cast<int>((R + kBucketCluster * 1024 - 1) / (kBucketCluster * 1024)) * 32;  // rows of a warp
+  const long long r0 = static_cast<long long>(rank * 32 + w) * run;
+  uint16_t* mine = wcnt + static_cast<size_t>(w) * N;
+  int e[kBucketClusterSteps];
+#pragma unroll
+  for (int s = 0; s < kBucketClusterSteps; ++s) {
+    const long long r = r0 + s * 32 + lane;
+    const int v = s * 32 < run && r < R ? idx[r] : -1;
+    e[s] = v >= 0 && v < N ? v : -1 - lane;  // no row: equal to no other
+    if (s * 32 < run && r < R && (v < 0 || v >= N)) report_error(BFMOE_EDEVICE_BOUNDS, static_cast<unsigned>(r));
+  }
+#pragma unroll
+  for (int s = 0; s < kBucketClusterSteps; ++s) {
+    if (s * 32 >= run) break;
+    const unsigned peers = __match_any_sync(FULL_MASK, e[s]);
+    if (e[s] >= 0 && lane == __ffs(peers) - 1) mine[e[s]] = static_cast<uint16_t>(mine[e[s]] + __popc(peers));
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int x = tid; x < N; x += 1024) {
+    int sum = 0;
+#pragma unroll 8
+    for (int q = 0; q < 32; ++q) {
+      const int c = wcnt[static_cast<size_t>(q) * N + x];
+      wcnt[static_cast<size_t>(q) * N + x] = static_cast<uint16_t>(sum);
+      sum += c;
+    }
+    tot[x] = sum;
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  for (int x = tid; x < N; x += 1024) {
+    const uint32_t here = smem_u32(tot + x);
+    int before = 0, all = 0;
+#pragma unroll
+    for (int q = 0; q < kBucketCluster; ++q) {
+      uint32_t there;
+      int c;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(here), "r"(q));
+      asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(c) : "r"(there) : "memory");
+      all += c;
+      before += q < rank ? c : 0;
+    }
+    base[x] = before;
+    off[x] = all;
+  }
+  // (no CTA leaves, or changes its totals, before the others have read them)
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  for (int x = tid; x < N; x += 1024) tot[x] = off[x];
+  __syncthreads();
+  block_exclusive_scan([&](int x) { return tot[x]; }, N, off);
+  if (rank == 0)
+    for (int x = tid; x <= N; x += 1024) {
+      offsets_out[x] = off[x];
+      if (x < N) counts_out[x] = tot[x];
+    }
+#pragma unroll
+  for (int s = 0; s < kBucketClusterSteps; ++s) {
+    if (s * 32 >= run) break;
+    const unsigned peers = __match_any_sync(FULL_MASK, e[s]);
+    int before = 0;
+    if (e[s] >= 0) {
+      before = mine[e[s]];
+      rows[off[e[s]] + base[e[s]] + before + __popc(peers & ((1u << lane) - 1u))] =
+          static_cast<int32_t>(r0 + s * 32 + lane);
+    }
+    __syncwarp();
+    if (e[s] >= 0 && lane == __ffs(peers) - 1) mine[e[s]] = static_cast<uint16_t>(before + __popc(peers));
+    __syncwarp();
+  }
+}
+
 }  // namespace bfmoe

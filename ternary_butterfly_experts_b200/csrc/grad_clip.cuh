@@ -5,7 +5,8 @@
 // nothing; the sums' order is fixed.  A norm that is not finite scales nothing.
 //
 // The list travels in the kernel's parameters (no copy to the device, nothing
-// to keep alive for a captured graph): kGradsPerLaunch tensors a launch.
+// to keep alive for a captured graph): up to kGradsPerLaunch tensors a launch,
+// or kGradsFew where they are enough (15 KB of parameters against 2).
 #pragma once
 #include "route.cuh"
 
@@ -19,6 +20,7 @@ namespace bfmoe {
 // four 16-byte loads a thread, the norm of 189 MB of bfloat16 took 47 us, half
 // of the copy bandwidth: between a block's chunks nothing was in flight.)
 constexpr int kGradsPerLaunch = 512;
+constexpr int kGradsFew = 64;
 constexpr int kGradConsumers = 512;
 constexpr int kGradThreads = kGradConsumers + 32;
 constexpr int kGradBlocks = 2;          // of an SM
@@ -31,12 +33,13 @@ constexpr int kGradMaxParts = 1024;     // partial sums of one call
 
 // A tensor is cut at 16-byte boundaries: its first chunk has up to 15 bytes
 // before the first one too (head elements), its last less than 16 bytes more.
-struct GradList {
-  const void* src[kGradsPerLaunch];
-  void* dst[kGradsPerLaunch];
-  long long len[kGradsPerLaunch];
-  int first[kGradsPerLaunch + 1];  // chunks before each tensor
-  uint8_t src_type[kGradsPerLaunch], dst_type[kGradsPerLaunch], head[kGradsPerLaunch];
+template <int MAX>
+struct GradListOf {
+  const void* src[MAX];
+  void* dst[MAX];
+  long long len[MAX];
+  int first[MAX + 1];  // chunks before each tensor
+  uint8_t src_type[MAX], dst_type[MAX], head[MAX];
   int n;
 };
 
@@ -45,12 +48,14 @@ inline int grad_head(const void* p, int type, long long len) {
   return static_cast<int>(std::min<long long>(bytes / (type == BFMOE_BF16 ? 2 : 4), len));
 }
 inline long long grad_chunks(const void* p, int type, long long len) {
-  const long long body = (len - grad_head(p, type, len)) * (type == BFMOE_BF16 ? 2 : 4);
-  return std::max(1LL, (body + kGradChunkBytes - 1) / kGradChunkBytes);
+  const long long chunk = kGradChunkBytes / (type == BFMOE_BF16 ? 2 : 4);
+  const long long body = len - grad_head(p, type, len);
+  return std::max(1LL, body / chunk + (body % chunk != 0));
 }
 
 // The tensor of chunk c: the last i with first[i] <= c.
-__device__ __forceinline__ int grad_of_chunk(const GradList& g, int c) {
+template <class G>
+__device__ __forceinline__ int grad_of_chunk(const G& g, int c) {
   int lo = 0, hi = g.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -75,8 +80,8 @@ struct GradChunk {
 // where it says so use(chunk, vectors) for every chunk, else the copies stop
 // there.  Every wait is bounded; after one that ran out all return, the
 // producer after its own copies.
-template <class R, class F>
-__device__ __forceinline__ void grad_stream(const GradList& g, int first, int step, int count, R&& ready, F&& use) {
+template <class G, class R, class F>
+__device__ __forceinline__ void grad_stream(const G& g, int first, int step, int count, R&& ready, F&& use) {
   extern __shared__ __align__(128) uint8_t grad_ring[];
   __shared__ uint64_t full[kGradStages], empty[kGradStages], go;
   __shared__ GradChunk meta[kGradStages];
@@ -220,7 +225,8 @@ __device__ __forceinline__ void square_vector(double (&s)[4], uint32_t& top, con
   }
 }
 
-__global__ __launch_bounds__(kGradThreads, kGradBlocks) void grad_norm_kernel(const __grid_constant__ GradList g,
+template <int MAX>
+__global__ __launch_bounds__(kGradThreads, kGradBlocks) void grad_norm_kernel(const __grid_constant__ GradListOf<MAX> g,
                                                                               double* __restrict__ part) {
   __shared__ double red[32];
   pdl_wait();
@@ -323,7 +329,8 @@ __device__ __forceinline__ void grad_scale_chunk(const GradChunk& m, const uint4
 
 // The chunks are taken from the last one on: what the norm read last is still
 // in L2.
-__global__ __launch_bounds__(kGradThreads, kGradBlocks) void grad_scale_kernel(const __grid_constant__ GradList g,
+template <int MAX>
+__global__ __launch_bounds__(kGradThreads, kGradBlocks) void grad_scale_kernel(const __grid_constant__ GradListOf<MAX> g,
                                                                                const double* __restrict__ part,
                                                                                int parts, int all_in_place,
                                                                                float max_norm,

@@ -163,14 +163,15 @@ int check_overlap(const char* what, const bfmoe_grad* g, int n) {
 }
 
 // Tensors [i0, i1) of the list as a kernel argument; empty ones are left out.
-void fill_list(const bfmoe_grad* g, int i0, int i1, GradList& out) {
+template <int MAX>
+void fill_list(const bfmoe_grad* g, int i0, int i1, GradListOf<MAX>& out) {
   out.n = 0;
   long long chunks = 0;
   for (int i = i0; i < i1; ++i) {
     if (g[i].len == 0) continue;
     const int q = out.n++;
     out.src[q] = g[i].grad;
-    out.dst[q] = g[i].out ? g[i].out : const_cast<void*>(g[i].grad);
+    out.dst[q] = g[i].out ? g[i].out : const_cast<void*>(static_cast<const void*>(g[i].grad));
     out.len[q] = g[i].len;
     out.src_type[q] = static_cast<uint8_t>(g[i].dtype);
     out.dst_type[q] = static_cast<uint8_t>(g[i].out ? g[i].out_dtype : g[i].dtype);
@@ -189,26 +190,53 @@ long long total_chunks(const bfmoe_grad* g, int n) {
 }
 
 // The squares of the whole list into part; *parts: how many partial sums.
+template <int MAX>
 int launch_norm(const char* what, const bfmoe_grad* g, int n, double* part, int* parts, cudaStream_t s) {
   *parts = 0;
   static std::atomic<uint64_t> done{0};
   if (needs_attr(done)) {
-    cudaError_t e = cudaFuncSetAttribute(grad_norm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem);
+    cudaError_t e = cudaFuncSetAttribute(grad_norm_kernel<MAX>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(grad_scale_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem);
+      e = cudaFuncSetAttribute(grad_scale_kernel<MAX>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem);
     if (e != cudaSuccess) return cuda_fail(e, what);
     attr_set(done);
   }
-  const int lists = (n + kGradsPerLaunch - 1) / kGradsPerLaunch;
+  const int lists = (n + MAX - 1) / MAX;
   const int cap = lists ? std::min(sm_count() * kGradBlocks, kGradMaxParts / lists) : 0;
-  GradList l;
+  GradListOf<MAX> l;
   for (int q = 0; q < lists; ++q) {
-    fill_list(g, q * kGradsPerLaunch, std::min(n, (q + 1) * kGradsPerLaunch), l);
+    fill_list(g, q * MAX, std::min(n, (q + 1) * MAX), l);
     if (l.first[l.n] == 0) continue;
     const int grid = std::min(l.first[l.n], cap);
-    const cudaError_t e = launch("grad_norm", s, [&] { pdl_launch(grad_norm_kernel, grid, kGradThreads, kGradSmem, s, l, part + *parts); });
+    const cudaError_t e = launch("grad_norm", s, [&] {
+      pdl_launch(grad_norm_kernel<MAX>, grid, kGradThreads, kGradSmem, s, l, part + *parts);
+    });
     if (e != cudaSuccess) return cuda_fail(e, what);
     *parts += grid;
+  }
+  return BFMOE_OK;
+}
+
+// Norm, then scaling.  *written: whether the norm has been.
+template <int MAX>
+int launch_clip(const bfmoe_grad* g, int n, float max_norm, float* norm, double* part, int* parts, bool* written,
+                cudaStream_t s) {
+  int rc = launch_norm<MAX>("grad_clip: launch", g, n, part, parts, s);
+  if (rc) return rc;
+  GradListOf<MAX> l;
+  for (int i0 = 0; i0 < n; i0 += MAX) {
+    fill_list(g, i0, std::min(n, i0 + MAX), l);
+    if (l.first[l.n] == 0) continue;
+    int in_place = 1;
+    for (int q = 0; q < l.n; ++q) in_place &= l.src[q] == l.dst[q];
+    const int grid = std::min(l.first[l.n], sm_count() * kGradBlocks);
+    float* out = *written ? nullptr : norm;  // once
+    const cudaError_t e = launch("grad_scale", s, [&] {
+      pdl_launch(grad_scale_kernel<MAX>, grid, kGradThreads, kGradSmem, s, l, static_cast<const double*>(part), *parts,
+                 in_place, max_norm, out);
+    });
+    if (e != cudaSuccess) return cuda_fail(e, "grad_clip: launch");
+    *written = true;
   }
   return BFMOE_OK;
 }
@@ -223,33 +251,33 @@ cudaError_t with_shape(int N, F&& f) {
   return f(RowShape<32, 32>{});
 }
 
-template <class S, int BY, bool GROUPED>
-cudaError_t launch_route_rows(Logits x, int T, int N, int k, const RouteCfg& cfg, const float* bias, int32_t* idx,
+template <class S, int BY, bool GROUPED, typename Tl>
+cudaError_t launch_route_rows(Logits<Tl> x, int T, int N, int k, const RouteCfg& cfg, const float* bias, int32_t* idx,
                               float* gates, cudaStream_t s) {
   int lsh = 0;  // 1 << lsh lanes take a group
   while (GROUPED && (2 << lsh) * cfg.n_groups <= S::LPR) ++lsh;
-  x.wide = wide_rows<S>(x.p, x.ld, N, x.bf16 != 0);
+  x.wide = wide_rows<S>(x.p, x.ld, N);
   const size_t floats = (BY != kByLogit ? S::MAXN : 0) + (GROUPED ? kRouteWarps * S::ROWS * kGroupSpace<S> : 0) +
-                        (x.wide ? kRouteWarps * RowFeed<S>::BUFFER / 4 : 0);
+                        (x.wide ? kRouteWarps * RowFeed<S, Tl>::BUFFER / 4 : 0);
   if (S::V > 8) {
     static std::atomic<uint64_t> done{0};
     if (needs_attr(done)) {
-      const cudaError_t e = cudaFuncSetAttribute(route_fast_kernel<S, BY, GROUPED>,
+      const cudaError_t e = cudaFuncSetAttribute(route_fast_kernel<S, Tl, BY, GROUPED>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 S::MAXN * 4 + kRouteWarps * (S::ROWS * kGroupSpace<S> * 4 + RowFeed<S>::BUFFER));
+                                                 S::MAXN * 4 + kRouteWarps * (S::ROWS * kGroupSpace<S> * 4 + RowFeed<S, Tl>::BUFFER));
       if (e != cudaSuccess) return e;
       attr_set(done);
     }
   }
   const int grid = grid_for(T, kRouteWarps * S::ROWS, sm_count() * kRouteBlocks<S>);
   return launch("route", s, [&] {
-    route_fast_kernel<S, BY, GROUPED><<<grid, kRouteWarps * 32, floats * sizeof(float), s>>>(x, T, N, k, cfg, bias, lsh,
-                                                                                             idx, gates);
+    pdl_launch(route_fast_kernel<S, Tl, BY, GROUPED>, grid, kRouteWarps * 32, floats * sizeof(float), s, x, T, N, k, cfg, bias,
+               lsh, idx, gates);
   });
 }
 
-template <class S>
-cudaError_t launch_route_shape(const Logits& x, int T, int N, int k, const RouteCfg& cfg, const float* bias,
+template <class S, typename Tl>
+cudaError_t launch_route_shape(const Logits<Tl>& x, int T, int N, int k, const RouteCfg& cfg, const float* bias,
                                int32_t* idx, float* gates, cudaStream_t s) {
   const bool grouped = cfg.top_groups < cfg.n_groups;
   if (!bias && !(grouped && cfg.group_score == BFMOE_GROUP_TOP2)) {
@@ -265,29 +293,30 @@ cudaError_t launch_route_shape(const Logits& x, int T, int N, int k, const Route
 }
 
 // A row's logits in the registers of 16 or 32 lanes up to 1024 experts.
-cudaError_t launch_route(const Logits& x, int T, int N, int k, const RouteCfg& cfg, const float* bias, int32_t* idx,
+template <typename Tl>
+cudaError_t launch_route(const Logits<Tl>& x, int T, int N, int k, const RouteCfg& cfg, const float* bias, int32_t* idx,
                          float* gates, cudaStream_t s) {
   if (N <= 1024)
     return with_shape(
         N, [&](auto shape) { return launch_route_shape<decltype(shape)>(x, T, N, k, cfg, bias, idx, gates, s); });
   return launch("route", s, [&] {
-    route_long_kernel<<<grid_for(T, kRouteWarps, sm_count() * 8), kRouteWarps * 32, 0, s>>>(x, T, N, k, cfg, bias, idx,
-                                                                                            gates);
+    pdl_launch(route_long_kernel<Tl>, grid_for(T, kRouteWarps, sm_count() * 8), kRouteWarps * 32, 0, s, x, T, N, k, cfg, bias,
+               idx, gates);
   });
 }
 
-template <class S, bool SIGMOID>
-cudaError_t launch_balance_rows(Logits x, int T, int N, int k, const int32_t* idx, float* part, double* zpart,
+template <class S, bool SIGMOID, typename Tl>
+cudaError_t launch_balance_rows(Logits<Tl> x, int T, int N, int k, const int32_t* idx, float* part, double* zpart,
                                 int32_t* loads, int* grid, cudaStream_t s) {
-  constexpr size_t most = std::max<size_t>(kGradWarps * S::MAXN * 4, kGradWarps * RowFeed<S>::BUFFER);
-  const auto kern = balance_rows_kernel<S, SIGMOID>;
+  constexpr size_t most = std::max<size_t>(kGradWarps * S::MAXN * 4, kGradWarps * RowFeed<S, Tl>::BUFFER);
+  const auto kern = balance_rows_kernel<S, Tl, SIGMOID>;
   static std::atomic<uint64_t> done{0};
   if (needs_attr(done)) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
     if (e != cudaSuccess) return e;
     attr_set(done);
   }
-  x.wide = wide_rows<S>(x.p, x.ld, N, x.bf16 != 0);
+  x.wide = wide_rows<S>(x.p, x.ld, N);
   // a warp takes several rows where there are enough, so that the sums that
   // are left to add up stay few
   *grid = grid_for(T, kGradWarps * S::ROWS * 2, std::min(kBalanceBlocks, sm_count() * 2));
@@ -296,7 +325,8 @@ cudaError_t launch_balance_rows(Logits x, int T, int N, int k, const int32_t* id
   });
 }
 
-cudaError_t launch_balance(Logits x, int T, int N, int k, bool sigmoid, const int32_t* idx, float* part, double* zpart,
+template <typename Tl>
+cudaError_t launch_balance(const Logits<Tl>& x, int T, int N, int k, bool sigmoid, const int32_t* idx, float* part, double* zpart,
                            int32_t* loads, int* grid, cudaStream_t s) {
   if (N <= 1024)
     return with_shape(N, [&](auto shape) {
@@ -306,37 +336,38 @@ cudaError_t launch_balance(Logits x, int T, int N, int k, bool sigmoid, const in
     });
   static std::atomic<uint64_t> done{0};
   if (needs_attr(done)) {
-    const cudaError_t e = cudaFuncSetAttribute(balance_long_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(balance_long_kernel<Tl>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (kGradWarps + 1) * BFMOE_MAX_EXPERTS * 4);
     if (e != cudaSuccess) return e;
     attr_set(done);
   }
   *grid = grid_for(T, kGradWarps, std::min(kBalanceBlocks, sm_count() * 2));
   return launch("balance_rows", s, [&] {
-    pdl_launch(balance_long_kernel, *grid, kGradWarps * 32, static_cast<size_t>(kGradWarps + 1) * N * 4, s, x, T, N, k,
+    pdl_launch(balance_long_kernel<Tl>, *grid, kGradWarps * 32, static_cast<size_t>(kGradWarps + 1) * N * 4, s, x, T, N, k,
                sigmoid ? 1 : 0, idx, part, zpart, loads);
   });
 }
 
-template <class S, bool SIGMOID>
-cudaError_t launch_backward_rows(Logits x, int T, int N, int k, const RouteCfg& cfg, RouteGrad g, cudaStream_t s) {
-  constexpr size_t base = S::MAXN * (1 + kGradWarps * S::ROWS) * 4, most = base + kGradWarps * RowFeed<S>::BUFFER;
-  const auto kern = route_backward_kernel<S, SIGMOID>;
+template <class S, bool SIGMOID, typename Tl>
+cudaError_t launch_backward_rows(Logits<Tl> x, int T, int N, int k, const RouteCfg& cfg, RouteGrad g, cudaStream_t s) {
+  constexpr size_t base = S::MAXN * (1 + kGradWarps * S::ROWS) * 4, most = base + kGradWarps * RowFeed<S, Tl>::BUFFER;
+  const auto kern = route_backward_kernel<S, Tl, SIGMOID>;
   static std::atomic<uint64_t> done{0};
   if (needs_attr(done)) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
     if (e != cudaSuccess) return e;
     attr_set(done);
   }
-  x.wide = wide_rows<S>(x.p, x.ld, N, x.bf16 != 0);
-  g.wide_out = wide_rows<S>(g.out, g.ld_out, N, x.bf16 != 0);
+  x.wide = wide_rows<S>(x.p, x.ld, N);
+  g.wide_out = wide_rows<S>(static_cast<const Tl*>(g.out), g.ld_out, N);
   const int grid = grid_for(T, kGradWarps * S::ROWS, sm_count() * kGradRowBlocks<S>);
   return launch("route_backward", s, [&] {
     pdl_launch(kern, grid, kGradWarps * 32, x.wide ? most : base, s, x, T, N, k, cfg, g);
   });
 }
 
-cudaError_t launch_route_backward(Logits x, int T, int N, int k, const RouteCfg& cfg, const RouteGrad& g,
+template <typename Tl>
+cudaError_t launch_route_backward(const Logits<Tl>& x, int T, int N, int k, const RouteCfg& cfg, const RouteGrad& g,
                                   cudaStream_t s) {
   if (N <= 1024)
     return with_shape(N, [&](auto shape) {
@@ -345,7 +376,7 @@ cudaError_t launch_route_backward(Logits x, int T, int N, int k, const RouteCfg&
       return launch_backward_rows<S, false>(x, T, N, k, cfg, g, s);
     });
   return launch("route_backward", s, [&] {
-    pdl_launch(route_backward_long_kernel, grid_for(T, kGradWarps, sm_count() * 8), kGradWarps * 32, 0, s, x, T, N, k,
+    pdl_launch(route_backward_long_kernel<Tl>, grid_for(T, kGradWarps, sm_count() * 8), kGradWarps * 32, 0, s, x, T, N, k,
                cfg, g);
   });
 }
@@ -382,7 +413,11 @@ int bfmoe_route(const void* logits, int dtype, int T, long long ld, int n_expert
   const RoutePlan p = make_route_plan(N, T, k);
   if (buckets && (rc = check_space("route", ws, ws_bytes, p.total))) return rc;
   const RouteCfg cfg = cfg_of(scoring);
-  e = launch_route(Logits{logits, ld, dtype == BFMOE_BF16, 0}, T, N, k, cfg, balance_bias, idx, gates, s);
+  e = dtype == BFMOE_BF16
+          ? launch_route(Logits<__nv_bfloat16>{static_cast<const __nv_bfloat16*>(logits), ld, 0}, T, N, k, cfg,
+                         balance_bias, idx, gates, s)
+          : launch_route(Logits<float>{static_cast<const float*>(logits), ld, 0}, T, N, k, cfg, balance_bias, idx,
+                         gates, s);
   if (e != cudaSuccess) return cuda_fail(e, "route: launch");
   if (!buckets) return ok();
   uint8_t* W = static_cast<uint8_t*>(ws);
@@ -417,8 +452,12 @@ int bfmoe_balance_loss(const void* logits, int dtype, int T, long long ld, int n
   double* zpart = reinterpret_cast<double*>(W + p.zpart);
   int32_t* loads = reinterpret_cast<int32_t*>(W + p.loads);
   int grid = 0;
-  e = launch_balance(Logits{logits, ld, dtype == BFMOE_BF16, 0}, T, N, k, score == BFMOE_SCORE_SIGMOID, idx, part, zpart,
-                     loads, &grid, s);
+  const bool sigmoid = score == BFMOE_SCORE_SIGMOID;
+  e = dtype == BFMOE_BF16
+          ? launch_balance(Logits<__nv_bfloat16>{static_cast<const __nv_bfloat16*>(logits), ld, 0}, T, N, k, sigmoid,
+                           idx, part, zpart, loads, &grid, s)
+          : launch_balance(Logits<float>{static_cast<const float*>(logits), ld, 0}, T, N, k, sigmoid, idx, part, zpart,
+                           loads, &grid, s);
   if (e != cudaSuccess) return cuda_fail(e, "balance_loss: launch");
   e = launch("balance_finish", s, [&] {
     pdl_launch(balance_finish_kernel, kFinishBlocks, kFinishThreads, 0, s, static_cast<const float*>(part),
@@ -445,7 +484,10 @@ int bfmoe_route_backward(const void* logits, int dtype, int T, long long ld, int
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const RouteCfg cfg = cfg_of(scoring);
   const RouteGrad g{idx, dgates, load, dloss, dlogits, ld_dlogits, 0};
-  const cudaError_t e = launch_route_backward(Logits{logits, ld, dtype == BFMOE_BF16, 0}, T, N, k, cfg, g, s);
+  const cudaError_t e =
+      dtype == BFMOE_BF16
+          ? launch_route_backward(Logits<__nv_bfloat16>{static_cast<const __nv_bfloat16*>(logits), ld, 0}, T, N, k, cfg, g, s)
+          : launch_route_backward(Logits<float>{static_cast<const float*>(logits), ld, 0}, T, N, k, cfg, g, s);
   if (e != cudaSuccess) return cuda_fail(e, "route_backward: launch");
   return ok();
 }
@@ -461,7 +503,9 @@ int bfmoe_grad_norm(const bfmoe_grad* grads, int n, float* norm, void* ws, size_
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   double* part = static_cast<double*>(ws);
   int parts = 0;
-  if ((rc = launch_norm("grad_norm: launch", grads, n, part, &parts, s))) return rc;
+  rc = n <= kGradsFew ? launch_norm<kGradsFew>("grad_norm: launch", grads, n, part, &parts, s)
+                      : launch_norm<kGradsPerLaunch>("grad_norm: launch", grads, n, part, &parts, s);
+  if (rc) return rc;
   const cudaError_t e = launch("grad_norm_finish", s, [&] { pdl_launch(grad_norm_finish_kernel, 1, kGradConsumers, 0, s, part, parts, norm); });
   if (e != cudaSuccess) return cuda_fail(e, "grad_norm: launch");
   return ok();
@@ -479,22 +523,14 @@ int bfmoe_grad_clip(const bfmoe_grad* grads, int n, float max_norm, float* norm,
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   double* part = static_cast<double*>(ws);
   int parts = 0;
-  if ((rc = launch_norm("grad_clip: launch", grads, n, part, &parts, s))) return rc;
-  cudaError_t e;
-  GradList l;
-  float* out_norm = norm;
-  for (int i0 = 0; i0 < n; i0 += kGradsPerLaunch) {
-    fill_list(grads, i0, std::min(n, i0 + kGradsPerLaunch), l);
-    if (l.first[l.n] == 0) continue;
-    int in_place = 1;
-    for (int q = 0; q < l.n; ++q) in_place &= l.src[q] == l.dst[q];
-    const int grid = std::min(l.first[l.n], sm_count() * kGradBlocks);
-    e = launch("grad_scale", s, [&] { pdl_launch(grad_scale_kernel, grid, kGradThreads, kGradSmem, s, l, part, parts, in_place, max_norm, out_norm); });
-    if (e != cudaSuccess) return cuda_fail(e, "grad_clip: launch");
-    out_norm = nullptr;  // written once
-  }
-  if (out_norm) {  // nothing to scale: the norm of an empty list
-    e = launch("grad_norm_finish", s, [&] { pdl_launch(grad_norm_finish_kernel, 1, kGradConsumers, 0, s, part, parts, norm); });
+  bool written = false;
+  rc = n <= kGradsFew ? launch_clip<kGradsFew>(grads, n, max_norm, norm, part, &parts, &written, s)
+                      : launch_clip<kGradsPerLaunch>(grads, n, max_norm, norm, part, &parts, &written, s);
+  if (rc) return rc;
+  if (!written) {  // nothing to scale: the norm of an empty list
+    const cudaError_t e = launch("grad_norm_finish", s, [&] {
+      pdl_launch(grad_norm_finish_kernel, 1, kGradConsumers, 0, s, static_cast<const double*>(part), parts, norm);
+    });
     if (e != cudaSuccess) return cuda_fail(e, "grad_clip: launch");
   }
   return ok();

@@ -79,16 +79,15 @@ __device__ __forceinline__ float unit_sigmoid(float l, float low) {
   return l > 0.f ? sigmoid_fast(l) : exp_fast(l - low) * rcp_fast(1.f + exp_fast(l));
 }
 
-// A matrix of logits of either type.
+// A matrix of logits.  (The type is a template parameter all the way down: a
+// test of it inside unrolled loops is predicated, and both sides are issued.)
+template <typename T>
 struct Logits {
-  const void* p;
+  static constexpr bool BF16 = sizeof(T) == 2;
+  const T* p;
   long long ld;
-  int bf16;
   int wide;  // rows are whole cells of 16-byte aligned memory (RowShape)
-  __device__ __forceinline__ float at(int t, int e) const {
-    const long long i = static_cast<long long>(t) * ld + e;
-    return bf16 ? to_f32(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
-  }
+  __device__ __forceinline__ float at(int t, int e) const { return to_f32(p[static_cast<long long>(t) * ld + e]); }
 };
 
 // The score of a logit that is not masked, in 64 bits: M and Z the row's
@@ -120,7 +119,8 @@ constexpr int kRouteWindow = 32;
 // the k-th is ranked again by its 64-bit value (win: kRouteWindow ints of the
 // warp's shared memory; more than that many: k passes over the whole row).
 // Lane j ends with the expert of slot j.
-__device__ __noinline__ void route_row_64(const Logits& x, int t, int N, int k, const RouteCfg& cfg,
+template <typename Tl>
+__device__ __noinline__ void route_row_64(const Logits<Tl>& x, int t, int N, int k, const RouteCfg& cfg,
                                           const float* __restrict__ bias, int* win, int lane, int& e_out,
                                           float& gate_out) {
   const bool softmax = cfg.score == BFMOE_SCORE_SOFTMAX;
@@ -361,91 +361,82 @@ struct RowShape {
 
 // A row's words as they are in memory, so that the next row can be on its way
 // while one is worked on.  Words behind the row's end are -inf of its type.
-template <class S>
+template <class S, typename Tl>
 struct RawRow {
-  uint32_t w[S::V];
-  __device__ __forceinline__ void load(const Logits& x, int t, int N, int q) {
-    const long long at = static_cast<long long>(t) * x.ld;
+  static constexpr bool BF16 = sizeof(Tl) == 2;
+  static constexpr int W = BF16 ? S::V / 2 : S::V;  // words
+  static constexpr int CW = W / S::C;               // of a cell: 2, 4 or 8
+  uint32_t w[W];
+
+  // A cell from 16-byte aligned (8-byte: CW = 2) memory, global or shared.
+  __device__ __forceinline__ void load_cell(int c, const Tl* p, bool in) {
+    constexpr uint32_t M = BF16 ? 0xff80ff80u : 0xff800000u;
+    if constexpr (CW == 2) {
+      const uint2 u = in ? *reinterpret_cast<const uint2*>(p) : make_uint2(M, M);
+      w[2 * c] = u.x, w[2 * c + 1] = u.y;
+    } else {
 #pragma unroll
-    for (int c = 0; c < S::C; ++c) {
-      const int e0 = (c * S::LPR + q) * S::CE;
-      uint32_t* v = w + c * S::CE;
-      if (x.wide) {
-        if (x.bf16) {
-          const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(x.p) + at + e0;
-          if constexpr (S::CE == 8) {
-            const uint4 u = e0 < N ? *reinterpret_cast<const uint4*>(p)
-                                   : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-            v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
-          } else {
-            const uint2 u = e0 < N ? *reinterpret_cast<const uint2*>(p) : make_uint2(0xff80ff80u, 0xff80ff80u);
-            v[0] = u.x, v[1] = u.y;
+      for (int h = 0; h < CW / 4; ++h) {
+        const uint4 u = in ? reinterpret_cast<const uint4*>(p)[h] : make_uint4(M, M, M, M);
+        w[CW * c + 4 * h] = u.x, w[CW * c + 4 * h + 1] = u.y;
+        w[CW * c + 4 * h + 2] = u.z, w[CW * c + 4 * h + 3] = u.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void load(const Logits<Tl>& x, int t, int N, int q) {
+    const Tl* row = x.p + static_cast<long long>(t) * x.ld;
+    if (x.wide) {
+#pragma unroll
+      for (int c = 0; c < S::C; ++c) {
+        const int e0 = (c * S::LPR + q) * S::CE;
+        load_cell(c, row + e0, e0 < N);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < S::C; ++c) {
+        const int e0 = (c * S::LPR + q) * S::CE;
+        if constexpr (BF16) {
+          const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
+#pragma unroll
+          for (int h = 0; h < CW; ++h) {
+            const int e = e0 + 2 * h;
+            const uint32_t a = e < N ? p[e] : 0xff80u, b = e + 1 < N ? p[e + 1] : 0xff80u;
+            w[CW * c + h] = a | b << 16;
           }
         } else {
-          const float* p = static_cast<const float*>(x.p) + at + e0;
+          const uint32_t* p = reinterpret_cast<const uint32_t*>(row);
 #pragma unroll
-          for (int h = 0; h < S::CE; h += 4) {
-            const uint4 u = e0 < N ? *reinterpret_cast<const uint4*>(p + h)
-                                   : make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
-            v[h] = u.x, v[h + 1] = u.y, v[h + 2] = u.z, v[h + 3] = u.w;
-          }
+          for (int h = 0; h < CW; ++h) w[CW * c + h] = e0 + h < N ? p[e0 + h] : 0xff800000u;
         }
-      } else if (x.bf16) {
-        const uint16_t* p = static_cast<const uint16_t*>(x.p) + at + e0;
-#pragma unroll
-        for (int h = 0; h < S::CE / 2; ++h) {
-          const uint32_t a = e0 + 2 * h < N ? p[2 * h] : 0xff80u, b = e0 + 2 * h + 1 < N ? p[2 * h + 1] : 0xff80u;
-          v[h] = a | b << 16;
-        }
-      } else {
-        const uint32_t* p = static_cast<const uint32_t*>(x.p) + at + e0;
-#pragma unroll
-        for (int i = 0; i < S::CE; ++i) v[i] = e0 + i < N ? p[i] : 0xff800000u;
       }
     }
   }
   // The same words from a copy of the row in shared memory.
-  __device__ __forceinline__ void load_shared(const uint8_t* row, bool bf16, int N, int q) {
+  __device__ __forceinline__ void load_shared(const uint8_t* row, int N, int q) {
 #pragma unroll
     for (int c = 0; c < S::C; ++c) {
       const int e0 = (c * S::LPR + q) * S::CE;
-      uint32_t* v = w + c * S::CE;
-      if (bf16) {
-        uint4 u = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-        if (e0 < N) u = *reinterpret_cast<const uint4*>(row + e0 * 2);
-        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
-      } else {
-#pragma unroll
-        for (int h = 0; h < S::CE; h += 4) {
-          uint4 u = make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
-          if (e0 < N) u = *reinterpret_cast<const uint4*>(row + (e0 + h) * 4);
-          v[h] = u.x, v[h + 1] = u.y, v[h + 2] = u.z, v[h + 3] = u.w;
-        }
-      }
+      load_cell(c, reinterpret_cast<const Tl*>(row) + e0, e0 < N);
     }
   }
   // The logits, NaN as -inf; of bfloat16, whose equal values meet as keys, -0
   // as 0.
-  __device__ __forceinline__ void unpack(bool bf16, float (&l)[S::V]) const {
+  __device__ __forceinline__ void unpack(float (&l)[S::V]) const {
 #pragma unroll
-    for (int c = 0; c < S::C; ++c) {
-      if (bf16) {
-#pragma unroll
-        for (int h = 0; h < S::CE / 2; ++h) {
-          l[c * S::CE + 2 * h] = fmaxf(__uint_as_float(w[c * S::CE + h] << 16), -INFINITY) + 0.f;
-          l[c * S::CE + 2 * h + 1] = fmaxf(__uint_as_float(w[c * S::CE + h] & 0xffff0000u), -INFINITY) + 0.f;
-        }
+    for (int i = 0; i < W; ++i) {
+      if constexpr (BF16) {
+        l[2 * i] = fmaxf(__uint_as_float(w[i] << 16), -INFINITY) + 0.f;
+        l[2 * i + 1] = fmaxf(__uint_as_float(w[i] & 0xffff0000u), -INFINITY) + 0.f;
       } else {
-#pragma unroll
-        for (int i = 0; i < S::CE; ++i) l[c * S::CE + i] = fmaxf(__uint_as_float(w[c * S::CE + i]), -INFINITY);
+        l[i] = fmaxf(__uint_as_float(w[i]), -INFINITY);
       }
     }
   }
 };
 // Whether rows can be read in cells (Logits::wide).
-template <class S>
-inline bool wide_rows(const void* p, long long ld, int N, bool bf16) {
-  const size_t bytes = std::min<size_t>(16, S::CE * (bf16 ? 2 : 4));
+template <class S, typename Tl>
+inline bool wide_rows(const Tl* p, long long ld, int N) {
+  const size_t bytes = std::min<size_t>(16, S::CE * sizeof(Tl));
   return N % S::CE == 0 && ld % S::CE == 0 && reinterpret_cast<uintptr_t>(p) % bytes == 0;
 }
 
@@ -461,25 +452,24 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // A warp's rows t0, t0 + step, ..., loads ahead of the work: rows of up to 256
 // experts as registers, longer ones (in cells) through two buffers of the warp
 // in shared memory.
-template <class S>
+template <class S, typename Tl>
 struct RowFeed {
   static constexpr bool AHEAD = S::V <= 8;
-  static constexpr int BUFFER = AHEAD ? 0 : 2 * S::MAXN * 4;  // bytes of shared memory of a warp
-  RawRow<S> raw;
+  static constexpr int BUFFER = AHEAD ? 0 : 2 * S::MAXN * static_cast<int>(sizeof(Tl));  // bytes of shared memory of a warp
+  RawRow<S, Tl> raw;
   uint8_t* buf;
   uint64_t* full;
   const uint8_t* here;  // the row in shared memory, or NULL
   int turn;
   bool staged;
 
-  __device__ __forceinline__ void fetch(const Logits& x, int t, int N, int b) {  // one lane
-    const int es = x.bf16 ? 2 : 4;
-    mbar_expect_tx(full + b, N * es);
-    bulk_load(buf + b * S::MAXN * 4, static_cast<const uint8_t*>(x.p) + static_cast<long long>(t) * x.ld * es, N * es,
-              full + b);
+  __device__ __forceinline__ void fetch(const Logits<Tl>& x, int t, int N, int b) {  // one lane
+    const int bytes = N * static_cast<int>(sizeof(Tl));
+    mbar_expect_tx(full + b, bytes);
+    bulk_load(buf + b * (BUFFER / 2), x.p + static_cast<long long>(t) * x.ld, bytes, full + b);
   }
   // bars: two of the warp's (not AHEAD)
-  __device__ __forceinline__ void start(const Logits& x, int t0, int T, int N, int lane, uint8_t* buffer, uint64_t* bars) {
+  __device__ __forceinline__ void start(const Logits<Tl>& x, int t0, int T, int N, int lane, uint8_t* buffer, uint64_t* bars) {
     here = nullptr;
     turn = 0;
     staged = !AHEAD && x.wide;
@@ -500,10 +490,10 @@ struct RowFeed {
   // The logits of the warp's rows at t0 (a row past the end: the last one's).
   // False after a copy that did not come, which is reported: then nothing of
   // the warp's is on its way any more.
-  __device__ __forceinline__ bool take(const Logits& x, int t0, int step, int T, int N, int lane, float (&l)[S::V]) {
+  __device__ __forceinline__ bool take(const Logits<Tl>& x, int t0, int step, int T, int N, int lane, float (&l)[S::V]) {
     const int q = lane & (S::LPR - 1);
     if constexpr (AHEAD) {
-      raw.unpack(x.bf16, l);
+      raw.unpack(l);
       if (t0 + step < T) raw.load(x, min(t0 + step + lane / S::LPR, T - 1), N, q);
     } else {
       if (staged) {
@@ -514,22 +504,20 @@ struct RowFeed {
           if (t0 + step < T) mbar_wait(full + (b ^ 1), ((turn + 1) >> 1) & 1, 0x2101u);
           return false;
         }
-        here = buf + b * S::MAXN * 4;
-        raw.load_shared(here, x.bf16, N, q);
+        here = buf + b * (BUFFER / 2);
+        raw.load_shared(here, N, q);
         __syncwarp();
         ++turn;
       } else {
         raw.load(x, min(t0 + lane / S::LPR, T - 1), N, q);
       }
-      raw.unpack(x.bf16, l);
+      raw.unpack(l);
     }
     return true;
   }
   // Logit e of row t, the row taken last.
-  __device__ __forceinline__ float at(const Logits& x, int t, int e) const {
-    if (!AHEAD && here)
-      return x.bf16 ? to_f32(reinterpret_cast<const __nv_bfloat16*>(here)[e]) : reinterpret_cast<const float*>(here)[e];
-    return x.at(t, e);
+  __device__ __forceinline__ float at(const Logits<Tl>& x, int t, int e) const {
+    return !AHEAD && here ? to_f32(reinterpret_cast<const Tl*>(here)[e]) : x.at(t, e);
   }
 };
 
@@ -580,9 +568,9 @@ constexpr int kGroupSpace = S::V <= 8 ? 2 * S::MAXN : S::MAXN;
 // values.  Longer lists than a row's lanes are left to the whole warp
 // (route_row_64).
 // Values that the keys hold exactly (bfloat16 logits) need no gap.
-template <class S, int BY, bool GROUPED>
+template <class S, typename Tl, int BY, bool GROUPED>
 __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_kernel(
-    const Logits x, int T, int N, int k, const RouteCfg cfg, const float* __restrict__ bias, int lsh,
+    const Logits<Tl> x, int T, int N, int k, const RouteCfg cfg, const float* __restrict__ bias, int lsh,
     int32_t* __restrict__ idx, float* __restrict__ gates) {
   constexpr int LPR = S::LPR, V = S::V, CE = S::CE, C = S::C;
   constexpr int B = S::IB + S::CB;
@@ -597,13 +585,15 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
   const int per = GROUPED ? N / cfg.n_groups : N;
   const bool cells = per % CE == 0;  // no cell lies in two groups
   float* gs = route_smem + (SCORED ? S::MAXN : 0) + (w * S::ROWS + lane / LPR) * kGroupSpace<S>;
+  pdl_wait();
+  pdl_trigger();
   if constexpr (SCORED) {
     for (int e = threadIdx.x; e < S::MAXN; e += blockDim.x)
       route_smem[e] = bias && e < N ? fmaxf(bias[e], -INFINITY) : 0.f;  // NaN masks
     __syncthreads();
   }
   const float eps_s = score_eps(softmax, V);
-  const bool exact_keys = x.bf16 && !bias;
+  const bool exact_keys = Logits<Tl>::BF16 && !bias;
   // groups: 1 << lsh lanes take one; lane q works on group gq (+ LPR, ...),
   // its cells begin in groups g0
   const int lpg = 1 << lsh, gq = q >> lsh;
@@ -617,11 +607,11 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
   const int step = gridDim.x * kRouteWarps * S::ROWS;
   int t0 = (blockIdx.x * kRouteWarps + w) * S::ROWS;
   __shared__ uint64_t full_s[kRouteWarps * 2];
-  RowFeed<S> feed;
+  RowFeed<S, Tl> feed;
   feed.start(x, t0, T, N, lane,
              reinterpret_cast<uint8_t*>(route_smem + (SCORED ? S::MAXN : 0) +
                                         (GROUPED ? kRouteWarps * S::ROWS * kGroupSpace<S> : 0)) +
-                 static_cast<size_t>(w) * RowFeed<S>::BUFFER,
+                 static_cast<size_t>(w) * RowFeed<S, Tl>::BUFFER,
              full_s + w * 2);
   for (; t0 < T; t0 += step) {
     const int t = min(t0 + lane / LPR, T - 1);
@@ -1015,13 +1005,16 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
 
 // Rows of more experts than registers hold: a warp a row, several passes over
 // it (it stays in the caches).
-__global__ __launch_bounds__(kRouteWarps * 32) void route_long_kernel(const Logits x, int T, int N, int k,
+template <typename Tl>
+__global__ __launch_bounds__(kRouteWarps * 32) void route_long_kernel(const Logits<Tl> x, int T, int N, int k,
                                                                       const RouteCfg cfg,
                                                                       const float* __restrict__ bias,
                                                                       int32_t* __restrict__ idx,
                                                                       float* __restrict__ gates) {
   __shared__ int win_s[kRouteWarps][kRouteWindow];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  pdl_wait();
+  pdl_trigger();
   for (int t = blockIdx.x * kRouteWarps + w; t < T; t += gridDim.x * kRouteWarps) {
     int e;
     float g;

@@ -32,21 +32,32 @@ struct TwoSided {
     t = l > 0.f ? e * r : r;
   }
 };
-// The row's sigmoids over exp(low) in u (low = min(m, 0)), and sigmoid(-l) in
-// t; masked logits give 0 and 1.
+// The row's sigmoids up to a factor of the row (shares need no more) in u,
+// sigmoid(-l) in t; masked logits give 0 and 1.  Where softmax terms x =
+// exp(l - m) are at hand and the largest logit is moderate, sigmoid(l) is
+// x / (x + exp(-m)): no second exponential.
 template <class S>
-__device__ __forceinline__ void row_sigmoid(const float (&l)[S::V], float m, float (&u)[S::V], float (&t)[S::V]) {
+__device__ __forceinline__ void row_sigmoid(const float (&l)[S::V], float m, bool has_x, const float (&x)[S::V],
+                                            float (&u)[S::V], float (&t)[S::V]) {
+  if (has_x && !__any_sync(FULL_MASK, !(m >= -10.f && m <= 40.f))) {
+    const float c = exp_fast(-m);
+#pragma unroll
+    for (int i = 0; i < S::V; ++i) {
+      const float r = rcp_fast(x[i] + c);
+      t[i] = c * r;
+      u[i] = x[i] * r;
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < S::V; ++i) {
     const TwoSided v(l[i]);
     u[i] = v.s;
     t[i] = v.t;
   }
-  if (__any_sync(FULL_MASK, m < 0.f)) {
-    if (m < 0.f && m > -INFINITY) {
+  if (m < 0.f && m > -INFINITY) {
 #pragma unroll
-      for (int i = 0; i < S::V; ++i) u[i] = masked_logit(l[i]) ? 0.f : exp_fast(l[i] - m) * t[i];
-    }
+    for (int i = 0; i < S::V; ++i) u[i] = masked_logit(l[i]) ? 0.f : exp_fast(l[i] - m) * t[i];
   }
 }
 template <class S>
@@ -72,9 +83,9 @@ __device__ __forceinline__ void load_cells(const float* a, int q, float (&v)[S::
 // rows, in a fixed order: part [grid][N] of p_te, zpart [grid] of lse^2, and
 // loads [grid][N + 1], the chosen slots of each expert and the rows.  A lane
 // keeps the sums of its experts in registers.
-template <class S, bool SIGMOID>
+template <class S, typename Tl, bool SIGMOID>
 __global__ __launch_bounds__(kGradWarps * 32, kGradRowBlocks<S>) void balance_rows_kernel(
-    const Logits x, int T, int N, int k, const int32_t* __restrict__ idx, float* __restrict__ part,
+    const Logits<Tl> x, int T, int N, int k, const int32_t* __restrict__ idx, float* __restrict__ part,
     double* __restrict__ zpart, int32_t* __restrict__ loads) {
   constexpr int LPR = S::LPR, V = S::V;
   extern __shared__ __align__(128) float grad_smem[];  // sums of a warp [kGradWarps][MAXN]; during the rows: their buffers
@@ -94,8 +105,8 @@ __global__ __launch_bounds__(kGradWarps * 32, kGradRowBlocks<S>) void balance_ro
   int rows = 0;
   const int step = gridDim.x * kGradWarps * S::ROWS;
   int t0 = (blockIdx.x * kGradWarps + w) * S::ROWS;
-  RowFeed<S> feed;
-  feed.start(x, t0, T, N, lane, reinterpret_cast<uint8_t*>(grad_smem) + static_cast<size_t>(w) * RowFeed<S>::BUFFER,
+  RowFeed<S, Tl> feed;
+  feed.start(x, t0, T, N, lane, reinterpret_cast<uint8_t*>(grad_smem) + static_cast<size_t>(w) * RowFeed<S, Tl>::BUFFER,
              full_s + w * 2);
   auto slot = [&](int t) { return q < k && t < T ? idx[static_cast<long long>(t) * k + q] : -1; };
   int e = slot(t0 + lane / LPR);
@@ -111,7 +122,7 @@ __global__ __launch_bounds__(kGradWarps * 32, kGradRowBlocks<S>) void balance_ro
     float inv;
     if constexpr (SIGMOID) {
       float c[V];
-      row_sigmoid<S>(l, m, u, c);
+      row_sigmoid<S>(l, m, true, u, u, c);
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) s += u[i];
@@ -178,7 +189,8 @@ __global__ __launch_bounds__(kGradWarps * 32, kGradRowBlocks<S>) void balance_ro
 struct RowSums {
   float m, z, s;  // largest logit, sum of unit_softmax, sum of unit_sigmoid
 };
-__device__ __forceinline__ RowSums row_sums(const Logits& x, int t, int N, int lane, bool sigmoid) {
+template <typename Tl>
+__device__ __forceinline__ RowSums row_sums(const Logits<Tl>& x, int t, int N, int lane, bool sigmoid) {
   RowSums r;
   float m = -INFINITY;
   for (int e = lane; e < N; e += 32) m = fmaxf(m, x.at(t, e));
@@ -197,7 +209,8 @@ __device__ __forceinline__ RowSums row_sums(const Logits& x, int t, int N, int l
 }
 
 // balance_rows_kernel for such rows: a warp a row, the sums in shared memory.
-__global__ __launch_bounds__(kGradWarps * 32) void balance_long_kernel(const Logits x, int T, int N, int k, int sig,
+template <typename Tl>
+__global__ __launch_bounds__(kGradWarps * 32) void balance_long_kernel(const Logits<Tl> x, int T, int N, int k, int sig,
                                                                        const int32_t* __restrict__ idx,
                                                                        float* __restrict__ part,
                                                                        double* __restrict__ zpart,
@@ -332,6 +345,24 @@ __global__ __cluster_dims__(kFinishBlocks, 1, 1) __launch_bounds__(kFinishThread
   }
 }
 
+// CE consecutive float32 values to an aligned cell.
+template <int CE>
+__device__ __forceinline__ void store_cell(float* p, const float* v) {
+#pragma unroll
+  for (int h = 0; h < CE; h += 4) *reinterpret_cast<float4*>(p + h) = make_float4(v[h], v[h + 1], v[h + 2], v[h + 3]);
+}
+template <int CE>
+__device__ __forceinline__ void store_cell(__nv_bfloat16* p, const float* v) {
+  uint32_t b[CE / 2];
+#pragma unroll
+  for (int h = 0; h < CE / 2; ++h) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * h], v[2 * h + 1]);
+    b[h] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+  if constexpr (CE == 8) *reinterpret_cast<uint4*>(p) = make_uint4(b[0], b[1], b[2], b[3]);
+  else *reinterpret_cast<uint2*>(p) = make_uint2(b[0], b[1]);
+}
+
 struct RouteGrad {
   const int32_t* idx;
   const float* dgates;   // or NULL
@@ -361,8 +392,8 @@ struct LossFactors {
 // losses and the plain softmax's gates (a_e = cb load_e, K the row's sums), and
 // each chosen expert has its own term, which reaches its lane through shared
 // memory.  Where only chosen experts have one, the row is not read.
-template <class S, bool SIGMOID>
-__global__ __launch_bounds__(kGradWarps * 32, kGradRowBlocks<S>) void route_backward_kernel(const Logits x, int T, int N,
+template <class S, typename Tl, bool SIGMOID>
+__global__ __launch_bounds__(kGradWarps * 32, kGradRowBlocks<S>) void route_backward_kernel(const Logits<Tl> x, int T, int N,
                                                                                             int k, const RouteCfg cfg,
                                                                                             const RouteGrad g) {
   constexpr int LPR = S::LPR, V = S::V;
@@ -382,11 +413,11 @@ __global__ __launch_bounds__(kGradWarps * 32, kGradRowBlocks<S>) void route_back
   const bool need_row = dense || f.cb != 0.f || f.cz != 0.f;
   const int step = gridDim.x * kGradWarps * S::ROWS;
   int t0 = (blockIdx.x * kGradWarps + w) * S::ROWS;
-  RowFeed<S> feed;
+  RowFeed<S, Tl> feed;
   if (need_row)
     feed.start(x, t0, T, N, lane,
                reinterpret_cast<uint8_t*>(grad_smem + S::MAXN * (1 + kGradWarps * S::ROWS)) +
-                   static_cast<size_t>(w) * RowFeed<S>::BUFFER,
+                   static_cast<size_t>(w) * RowFeed<S, Tl>::BUFFER,
                full_s + w * 2);
   else
     feed.here = nullptr;
@@ -430,7 +461,7 @@ __global__ __launch_bounds__(kGradWarps * 32, kGradRowBlocks<S>) void route_back
           const float z = row_softmax<S>(l, m, u);
           lse = m > -INFINITY ? row_lse(m, z) * f.cz * rcp_fast(z) : 0.f;
         }
-        row_sigmoid<S>(l, m, u, tt);
+        row_sigmoid<S>(l, m, f.cz != 0.f, u, u, tt);
 #pragma unroll
         for (int i = 0; i < V; ++i) s += u[i];
         s = seg_sum<LPR>(s);
@@ -498,42 +529,35 @@ __global__ __launch_bounds__(kGradWarps * 32, kGradRowBlocks<S>) void route_back
         for (int i = 0; i < V; ++i) o[i] = fmaf(u[i] * inv, a[i] + K, o[i]);
       }
     }
-    if (has) {
-      const long long at = static_cast<long long>(t) * g.ld_out;
+    Tl* row_out = static_cast<Tl*>(g.out) + static_cast<long long>(t) * g.ld_out;
+    if (g.wide_out) {
+      if (has) {
 #pragma unroll
-      for (int c = 0; c < S::C; ++c) {
-        const int e0 = (c * LPR + q) * S::CE;
-        const float* v = o + c * S::CE;
-        if (g.wide_out) {
-          if (e0 < N) {
-            if (x.bf16) {
-              uint32_t b[S::CE / 2];
-#pragma unroll
-              for (int h = 0; h < S::CE / 2; ++h) {
-                const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * h], v[2 * h + 1]);
-                b[h] = *reinterpret_cast<const uint32_t*>(&p);
-              }
-              auto* p = static_cast<__nv_bfloat16*>(g.out) + at + e0;
-              if constexpr (S::CE == 8) *reinterpret_cast<uint4*>(p) = make_uint4(b[0], b[1], b[2], b[3]);
-              else *reinterpret_cast<uint2*>(p) = make_uint2(b[0], b[1]);
-            } else {
-#pragma unroll
-              for (int h = 0; h < S::CE; h += 4)
-                *reinterpret_cast<float4*>(static_cast<float*>(g.out) + at + e0 + h) =
-                    make_float4(v[h], v[h + 1], v[h + 2], v[h + 3]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < S::CE; ++i)
-            if (e0 + i < N) {
-              if (x.bf16) static_cast<__nv_bfloat16*>(g.out)[at + e0 + i] = __float2bfloat16_rn(v[i]);
-              else static_cast<float*>(g.out)[at + e0 + i] = v[i];
-            }
+        for (int c = 0; c < S::C; ++c) {
+          const int e0 = (c * LPR + q) * S::CE;
+          if (e0 < N) store_cell<S::CE>(row_out + e0, o + c * S::CE);
         }
       }
+    } else {
+      // rows that are not aligned: through shared memory, so that neighbouring
+      // lanes write neighbouring elements (each lane its own cell's, the 33 MB
+      // of 16383 x 250 gradients took 28 us)
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < S::C; ++c)
+#pragma unroll
+        for (int h = 0; h < S::CE; h += 4) {
+          const float* v = o + c * S::CE + h;
+          *reinterpret_cast<float4*>(mine + (c * LPR + q) * S::CE + h) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+      __syncwarp();
+      for (int i = q; i < N; i += LPR) {
+        if (has) row_out[i] = from_f32<Tl>(mine[i]);
+        mine[i] = 0.f;
+      }
+      __syncwarp();
     }
-    if (g.dgates) {  // every lane has read its cells
+    if (g.dgates && g.wide_out) {  // every lane has read its cells
       __syncwarp();
       if (e >= 0) mine[e] = 0.f;
       __syncwarp();
@@ -542,7 +566,8 @@ __global__ __launch_bounds__(kGradWarps * 32, kGradRowBlocks<S>) void route_back
 }
 
 // Rows of more experts than registers hold: a warp a row, several passes.
-__global__ __launch_bounds__(kGradWarps * 32) void route_backward_long_kernel(const Logits x, int T, int N, int k,
+template <typename Tl>
+__global__ __launch_bounds__(kGradWarps * 32) void route_backward_long_kernel(const Logits<Tl> x, int T, int N, int k,
                                                                               const RouteCfg cfg, const RouteGrad g) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   pdl_wait();
@@ -619,8 +644,7 @@ __global__ __launch_bounds__(kGradWarps * 32) void route_backward_long_kernel(co
       }
       if (q < N) {
         const long long at = static_cast<long long>(t) * g.ld_out + q;
-        if (x.bf16) static_cast<__nv_bfloat16*>(g.out)[at] = __float2bfloat16_rn(o);
-        else static_cast<float*>(g.out)[at] = o;
+        static_cast<Tl*>(g.out)[at] = from_f32<Tl>(o);
       }
     }
     __syncwarp();
