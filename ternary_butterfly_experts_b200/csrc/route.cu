@@ -255,21 +255,21 @@ template <class S, int BY, bool GROUPED, typename Tl>
 cudaError_t launch_route_rows(Logits<Tl> x, int T, int N, int k, const RouteCfg& cfg, const float* bias, int32_t* idx,
                               float* gates, cudaStream_t s) {
   int lsh = 0;  // 1 << lsh lanes take a group
-  while (GROUPED && (2 << lsh) * cfg.n_groups <= S::LPR) ++lsh;
+  while (GROUPED && (2 << lsh) * cfg.n_groups <= 32) ++lsh;
   x.wide = wide_rows<S>(x.p, x.ld, N);
-  const size_t floats = (BY != kByLogit ? S::MAXN : 0) + (GROUPED ? kRouteWarps * S::ROWS * kGroupSpace<S> : 0) +
+  const size_t floats = (BY != kByLogit ? S::MAXN : 0) + (GROUPED ? kRouteWarps * kGroupSpace<S> : 0) +
                         (x.wide ? kRouteWarps * RowFeed<S, Tl>::BUFFER / 4 : 0);
   if (S::V > 8) {
     static std::atomic<uint64_t> done{0};
     if (needs_attr(done)) {
       const cudaError_t e = cudaFuncSetAttribute(route_fast_kernel<S, Tl, BY, GROUPED>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 S::MAXN * 4 + kRouteWarps * (S::ROWS * kGroupSpace<S> * 4 + RowFeed<S, Tl>::BUFFER));
+                                                 S::MAXN * 4 + kRouteWarps * (kGroupSpace<S> * 4 + RowFeed<S, Tl>::BUFFER));
       if (e != cudaSuccess) return e;
       attr_set(done);
     }
   }
-  const int grid = grid_for(T, kRouteWarps * S::ROWS, sm_count() * kRouteBlocks<S>);
+  const int grid = grid_for(T, kRouteWarps, sm_count() * kRouteBlocks<S>);
   return launch("route", s, [&] {
     pdl_launch(route_fast_kernel<S, Tl, BY, GROUPED>, grid, kRouteWarps * 32, floats * sizeof(float), s, x, T, N, k, cfg, bias,
                lsh, idx, gates);
@@ -292,13 +292,15 @@ cudaError_t launch_route_shape(const Logits<Tl>& x, int T, int N, int k, const R
   return launch_route_rows<S, kBySigmoid, false>(x, T, N, k, cfg, bias, idx, gates, s);
 }
 
-// A row's logits in the registers of 16 or 32 lanes up to 1024 experts.
+// A row's logits in the registers of a warp up to 1024 experts.
 template <typename Tl>
 cudaError_t launch_route(const Logits<Tl>& x, int T, int N, int k, const RouteCfg& cfg, const float* bias, int32_t* idx,
                          float* gates, cudaStream_t s) {
-  if (N <= 1024)
-    return with_shape(
-        N, [&](auto shape) { return launch_route_shape<decltype(shape)>(x, T, N, k, cfg, bias, idx, gates, s); });
+  if (N <= 64) return launch_route_shape<RowShape<32, 2>>(x, T, N, k, cfg, bias, idx, gates, s);
+  if (N <= 128) return launch_route_shape<RowShape<32, 4>>(x, T, N, k, cfg, bias, idx, gates, s);
+  if (N <= 256) return launch_route_shape<RowShape<32, 8>>(x, T, N, k, cfg, bias, idx, gates, s);
+  if (N <= 512) return launch_route_shape<RowShape<32, 16>>(x, T, N, k, cfg, bias, idx, gates, s);
+  if (N <= 1024) return launch_route_shape<RowShape<32, 32>>(x, T, N, k, cfg, bias, idx, gates, s);
   return launch("route", s, [&] {
     pdl_launch(route_long_kernel<Tl>, grid_for(T, kRouteWarps, sm_count() * 8), kRouteWarps * 32, 0, s, x, T, N, k, cfg, bias,
                idx, gates);

@@ -352,11 +352,9 @@ struct RowShape {
   static constexpr int LPR = LPR_, V = V_;
   static constexpr int CE = V < 8 ? V : 8;
   static constexpr int C = V / CE;
-  static constexpr int IB = CE == 8 ? 3 : 2;
-  static constexpr int CB = C == 4 ? 2 : (C == 2 ? 1 : 0);
   static constexpr int ROWS = 32 / LPR;  // rows of a warp
   static constexpr int MAXN = LPR * V;
-  static_assert(CE >= 4 && C <= 4);
+  static_assert(CE >= 2 && C <= 4);
 };
 
 // A row's words as they are in memory, so that the next row can be on its way
@@ -365,13 +363,16 @@ template <class S, typename Tl>
 struct RawRow {
   static constexpr bool BF16 = sizeof(Tl) == 2;
   static constexpr int W = BF16 ? S::V / 2 : S::V;  // words
-  static constexpr int CW = W / S::C;               // of a cell: 2, 4 or 8
+  static constexpr int CW = W / S::C;               // of a cell: 1, 2, 4 or 8
   uint32_t w[W];
 
-  // A cell from 16-byte aligned (8-byte: CW = 2) memory, global or shared.
+  // A cell from aligned memory (to 16 bytes, or a smaller cell), global or
+  // shared.
   __device__ __forceinline__ void load_cell(int c, const Tl* p, bool in) {
     constexpr uint32_t M = BF16 ? 0xff80ff80u : 0xff800000u;
-    if constexpr (CW == 2) {
+    if constexpr (CW == 1) {
+      w[c] = in ? *reinterpret_cast<const uint32_t*>(p) : M;
+    } else if constexpr (CW == 2) {
       const uint2 u = in ? *reinterpret_cast<const uint2*>(p) : make_uint2(M, M);
       w[2 * c] = u.x, w[2 * c + 1] = u.y;
     } else {
@@ -411,13 +412,11 @@ struct RawRow {
       }
     }
   }
-  // The same words from a copy of the row in shared memory.
-  __device__ __forceinline__ void load_shared(const uint8_t* row, int N, int q) {
+  // The same words from a copy of the row in shared memory (all MAXN of it).
+  __device__ __forceinline__ void load_shared(const uint8_t* row, int q) {
 #pragma unroll
-    for (int c = 0; c < S::C; ++c) {
-      const int e0 = (c * S::LPR + q) * S::CE;
-      load_cell(c, reinterpret_cast<const Tl*>(row) + e0, e0 < N);
-    }
+    for (int c = 0; c < S::C; ++c)
+      load_cell(c, reinterpret_cast<const Tl*>(row) + (c * S::LPR + q) * S::CE, true);
   }
   // The logits, NaN as -inf; of bfloat16, whose equal values meet as keys, -0
   // as 0.
@@ -478,6 +477,9 @@ struct RowFeed {
     if constexpr (AHEAD) {
       if (t0 < T) raw.load(x, min(t0 + lane / S::LPR, T - 1), N, lane & (S::LPR - 1));
     } else if (staged) {
+      // behind the row's end the buffers hold -inf, which no copy reaches
+      for (int e = N + lane; e < S::MAXN; e += 32)
+        for (int b = 0; b < 2; ++b) reinterpret_cast<Tl*>(buf + b * (BUFFER / 2))[e] = from_f32<Tl>(-INFINITY);
       if (lane == 0) {
         mbar_init(full, 1);
         mbar_init(full + 1, 1);
@@ -505,7 +507,7 @@ struct RowFeed {
           return false;
         }
         here = buf + b * (BUFFER / 2);
-        raw.load_shared(here, N, q);
+        raw.load_shared(here, q);
         __syncwarp();
         ++turn;
       } else {
@@ -538,53 +540,81 @@ __device__ __forceinline__ float row_softmax(const float (&l)[S::V], float m, fl
   return seg_sum<S::LPR>(z);
 }
 
+template <class S>
+__device__ __forceinline__ float row_max(const float (&l)[S::V]) {
+  float h = l[0];
+#pragma unroll
+  for (int i = 1; i < S::V; ++i) h = fmaxf(h, l[i]);
+  return seg_max<S::LPR>(h);
+}
+// A lane's cells from an array in shared memory.
+template <class S>
+__device__ __forceinline__ void load_cells(const float* a, int q, float (&v)[S::V]) {
+  if constexpr (S::CE == 2) {
+    const float2 f = *reinterpret_cast<const float2*>(a + q * 2);
+    v[0] = f.x, v[1] = f.y;
+  } else {
+#pragma unroll
+    for (int c = 0; c < S::C; ++c)
+#pragma unroll
+      for (int h = 0; h < S::CE; h += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(a + (c * S::LPR + q) * S::CE + h);
+        v[c * S::CE + h] = f.x, v[c * S::CE + h + 1] = f.y, v[c * S::CE + h + 2] = f.z, v[c * S::CE + h + 3] = f.w;
+      }
+  }
+}
+
 // What ranks the experts: the logits, or softmax or sigmoid scores (with a
 // bias, or summed up by group).
 enum { kByLogit = 0, kBySoftmax = 1, kBySigmoid = 2 };
 
 // Blocks of an SM: what the registers of a row leave room for.
 template <class S>
-constexpr int kRouteBlocks = S::V <= 8 ? 4 : (S::V <= 16 ? 3 : 2);
+constexpr int kRouteBlocks = S::V <= 8 ? 4 : 3;
 
 // Floats of shared memory for the group values of a row: all values in 64 bits
 // where there is room for them.
 template <class S>
 constexpr int kGroupSpace = S::V <= 8 ? 2 * S::MAXN : S::MAXN;
 
-// A row in the registers of LPR lanes, N <= LPR * V.
+// A candidate of a row.
+struct Candidate {
+  float value;
+  int e;
+  float eps;  // error of the value
+  int pad;
+};
+
+// A warp a row, the row in its registers (N <= 32 V).
 //
-// Ranking.  A value becomes a 32-bit key: its bits in integer order, the last
-// B of them replaced by its place in the lane (the lower the expert, the
-// larger), so that a lane's keys differ and its largest names its expert.  A
-// pick is one warp-wide integer maximum of the lanes' largest keys without
-// the place inside a cell; among equal ones the lowest lane has the lowest
-// expert.  The lane that was picked finds its next key by one pass over its
-// cell: max(key - picked) in wrapping arithmetic is the largest key below the
-// picked one, and no key has to be moved.
-// The truncated keys and the float32 scores rank two values rightly when they
-// are further apart than both errors; k + 1 picks are taken and every gap is
-// looked at.  A row with a smaller gap (about 1 in 1000) takes more picks until
-// a clear gap closes the list, whose experts are then ranked by their 64-bit
-// values.  Longer lists than a row's lanes are left to the whole warp
-// (route_row_64).
-// Values that the keys hold exactly (bfloat16 logits) need no gap.
+// Choice.  The (k + 1)-th largest of the lanes' maxima is at most the
+// (k + 1)-th largest value of the row, and few values reach it (about 10 of
+// 256 or 1024 for k = 8): those are the candidates, one a lane, ranked among
+// each other by value and index.  (Picking the largest k + 1 times instead,
+// with every value made into a sortable key, took 820 instructions a row of
+// 1024 experts for k = 4; this takes half.)
+// A row with more than 32 candidates (many equal values) is left to
+// route_row_64.
+//
+// Scores are float32 and rank two values rightly only where they are further
+// apart than their errors.  The threshold is lowered by both, and where two
+// candidates are nearer (about 1 row in 1000) they are ranked by 64-bit values.
+// Groups that are too near each other are treated alike.
 template <class S, typename Tl, int BY, bool GROUPED>
 __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_kernel(
     const Logits<Tl> x, int T, int N, int k, const RouteCfg cfg, const float* __restrict__ bias, int lsh,
     int32_t* __restrict__ idx, float* __restrict__ gates) {
-  constexpr int LPR = S::LPR, V = S::V, CE = S::CE, C = S::C;
-  constexpr int B = S::IB + S::CB;
-  constexpr uint32_t LOW = (1u << B) - 1u;
-  constexpr uint32_t MASKED = 0x007fffffu & ~LOW;  // ordered(-inf): above 0, below every value
+  constexpr int LPR = 32, V = S::V, CE = S::CE, C = S::C;
+  static_assert(S::LPR == 32);
   constexpr bool SCORED = BY != kByLogit;
   extern __shared__ __align__(128) float route_smem[];  // bias [MAXN] (scored), group values (grouped), rows
-  __shared__ int win_s[kRouteWarps][kRouteWindow];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int q = lane & (LPR - 1);
+  __shared__ Candidate cand_s[kRouteWarps][32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, q = lane;
   const bool softmax = BY == kBySoftmax || (BY == kByLogit && cfg.score == BFMOE_SCORE_SOFTMAX);
   const int per = GROUPED ? N / cfg.n_groups : N;
   const bool cells = per % CE == 0;  // no cell lies in two groups
-  float* gs = route_smem + (SCORED ? S::MAXN : 0) + (w * S::ROWS + lane / LPR) * kGroupSpace<S>;
+  float* gs = route_smem + (SCORED ? S::MAXN : 0) + w * kGroupSpace<S>;
+  Candidate* cand = cand_s[w];
   pdl_wait();
   pdl_trigger();
   if constexpr (SCORED) {
@@ -593,8 +623,7 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
     __syncthreads();
   }
   const float eps_s = score_eps(softmax, V);
-  const bool exact_keys = Logits<Tl>::BF16 && !bias;
-  // groups: 1 << lsh lanes take one; lane q works on group gq (+ LPR, ...),
+  // groups: 1 << lsh lanes take one; lane q works on group gq (+ 32, ...),
   // its cells begin in groups g0
   const int lpg = 1 << lsh, gq = q >> lsh;
   int g0[C];
@@ -604,44 +633,30 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
   }
   const int items = cells ? per / CE : per;  // of a group
 
-  const int step = gridDim.x * kRouteWarps * S::ROWS;
-  int t0 = (blockIdx.x * kRouteWarps + w) * S::ROWS;
+  const int step = gridDim.x * kRouteWarps;
+  int t = blockIdx.x * kRouteWarps + w;
   __shared__ uint64_t full_s[kRouteWarps * 2];
   RowFeed<S, Tl> feed;
-  feed.start(x, t0, T, N, lane,
-             reinterpret_cast<uint8_t*>(route_smem + (SCORED ? S::MAXN : 0) +
-                                        (GROUPED ? kRouteWarps * S::ROWS * kGroupSpace<S> : 0)) +
+  feed.start(x, t, T, N, lane,
+             reinterpret_cast<uint8_t*>(route_smem + (SCORED ? S::MAXN : 0) + (GROUPED ? kRouteWarps * kGroupSpace<S> : 0)) +
                  static_cast<size_t>(w) * RowFeed<S, Tl>::BUFFER,
              full_s + w * 2);
-  for (; t0 < T; t0 += step) {
-    const int t = min(t0 + lane / LPR, T - 1);
-    const bool has = t0 + lane / LPR < T;
+  for (; t < T; t += step) {
     float l[V], c[V];
-    if (!feed.take(x, t0, step, T, N, lane, l)) return;
+    if (!feed.take(x, t, step, T, N, lane, l)) return;
     float m = 0.f, inv_z = 1.f;
     if constexpr (BY == kBySoftmax) {
-      float h = l[0];
-#pragma unroll
-      for (int i = 1; i < V; ++i) h = fmaxf(h, l[i]);
-      m = seg_max<LPR>(h);
+      m = row_max<S>(l);
       const float z = row_softmax<S>(l, m, c);
       inv_z = z > 0.f ? rcp_fast(z) : 0.f;
     }
     if constexpr (SCORED) {
+      float b[V];
+      load_cells<S>(route_smem, q, b);
 #pragma unroll
-      for (int cc = 0; cc < C; ++cc) {
-        const int e0 = (cc * LPR + q) * CE;
-#pragma unroll
-        for (int h = 0; h < CE; h += 4) {
-          const float4 b = *reinterpret_cast<const float4*>(route_smem + e0 + h);
-          const float bb[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int v = cc * CE + h + i;
-            const float s = BY == kBySoftmax ? fmaf(c[v], inv_z, bb[i]) : sigmoid_fast(l[v]) + bb[i];
-            c[v] = masked_logit(l[v]) ? -INFINITY : s;
-          }
-        }
+      for (int v = 0; v < V; ++v) {
+        const float s = BY == kBySoftmax ? fmaf(c[v], inv_z, b[v]) : sigmoid_fast(l[v]) + b[v];
+        c[v] = masked_logit(l[v]) ? -INFINITY : s;
       }
     } else {
 #pragma unroll
@@ -815,165 +830,144 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
         }
       }
     }
-    // keys: 0 for what is no candidate
-    uint32_t key[V], head[C];
+    // what is no candidate: the other groups, and nothing behind the row's end
+    unsigned allowed = V == 32 ? 0xffffffffu : (1u << V) - 1u;
+    if (GROUPED || N < S::MAXN) {
+      allowed = 0u;
 #pragma unroll
-    for (int cc = 0; cc < C; ++cc) {
+      for (int cc = 0; cc < C; ++cc) {
+        const int e0 = (cc * LPR + q) * CE;
+        unsigned in = e0 + CE <= N ? (1u << CE) - 1u : (e0 < N ? (1u << (N - e0)) - 1u : 0u);
+        if constexpr (GROUPED) {
+          if (cells) {
+            if (!((kept >> (g0[cc] << lsh)) & 1ull)) in = 0u;
+          } else if (in) {
+            int g = g0[cc], r = e0 - g * per;
+            bool on = (kept >> (g << lsh)) & 1ull;
 #pragma unroll
-      for (int i = 0; i < CE; ++i) {
-        const uint32_t low = static_cast<uint32_t>((C - 1 - cc) * CE + (CE - 1 - i));
-        key[cc * CE + i] = (ordered(c[cc * CE + i]) & ~LOW) | low;
-      }
-      const int e0 = (cc * LPR + q) * CE;
-      if (N < S::MAXN) {
-#pragma unroll
-        for (int i = 0; i < CE; ++i)
-          if (e0 + i >= N) key[cc * CE + i] = 0u;
-      }
-      if constexpr (GROUPED) {
-        bool in = e0 < N && ((kept >> (g0[cc] << lsh)) & 1ull);
-        if (cells) {
-#pragma unroll
-          for (int i = 0; i < CE; ++i) key[cc * CE + i] = in ? key[cc * CE + i] : 0u;
-        } else {
-          int g = g0[cc], r = e0 - g * per;
-#pragma unroll
-          for (int i = 0; i < CE; ++i) {
-            if (r == per) {
-              r = 0;
-              ++g;
-              in = e0 + i < N && ((kept >> (g << lsh)) & 1ull);
+            for (int i = 0; i < CE; ++i) {
+              if (r == per) {
+                r = 0;
+                ++g;
+                on = e0 + i < N && ((kept >> (g << lsh)) & 1ull);
+              }
+              ++r;
+              if (!on) in &= ~(1u << i);
             }
-            ++r;
-            key[cc * CE + i] = in ? key[cc * CE + i] : 0u;
           }
         }
+        allowed |= in << (cc * CE);
       }
-      head[cc] = key[cc * CE];
-#pragma unroll
-      for (int i = 1; i < CE; ++i) head[cc] = max(head[cc], key[cc * CE + i]);
     }
+    if constexpr (GROUPED) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (!((allowed >> i) & 1u)) c[i] = -INFINITY;
+    }
+    float h = c[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) h = fmaxf(h, c[i]);
+    // threshold
+    const uint32_t first = ordered(h);
+    uint32_t key = first, last = 0u;
+#pragma unroll 1
+    for (int have = 0; have <= k;) {
+      last = __reduce_max_sync(FULL_MASK, key);
+      have += __popc(__ballot_sync(FULL_MASK, key == last));
+      if (key == last) key = 0u;
+    }
+    float least = from_ordered(last);
+    if (least == -INFINITY && N > 32) {
+      // what is left of the row lies in few lanes (groups, masks): the same
+      // over all values
+      float top = INFINITY;
+#pragma unroll 1
+      for (int have = 0; have <= k;) {
+        float v = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (c[i] < top || have == 0) v = fmaxf(v, c[i]);
+        top = seg_max<LPR>(v);
+        if (top == -INFINITY) break;
+        int equal = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) equal += c[i] == top;
+        have += __reduce_add_sync(FULL_MASK, equal);
+      }
+      least = top;
+    }
+    if constexpr (SCORED) {
+      if (bias && least < INFINITY) least -= 2.f * value_eps(eps_s, softmax, 1.f, least);
+    }
+    unsigned want = 0u;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (c[i] >= least) want |= 1u << i;
+    want &= allowed;
+    // candidates into lanes
+    int n = 0;
+    for (;;) {
+      const unsigned b = __ballot_sync(FULL_MASK, want != 0u);
+      if (!b) break;
+      const int at = n + __popc(b & ((1u << lane) - 1u));
+      if (want) {
+        const int i = __ffs(want) - 1;
+        if (at < 32) cand[at].e = ((i / CE) * LPR + lane) * CE + i % CE;
+        want &= want - 1u;
+      }
+      n += __popc(b);
+      if (n > 32) break;
+    }
+    __syncwarp();
+    clear = clear && n <= 32;
+    n = min(n, 32);
     if constexpr (BY == kByLogit) {
       if (softmax && !cfg.renorm) {
-        // any value near the largest serves as the maximum: a truncated key's
-        // (off by |m| 2^(B - 23)), unless it is large or not the row's (groups)
-        uint32_t top = head[0];
-#pragma unroll
-        for (int cc = 1; cc < C; ++cc) top = max(top, head[cc]);
-        m = from_ordered(seg_max_u32<LPR>(top) & ~LOW);
-        if (GROUPED || __any_sync(FULL_MASK, !(fabsf(m) < 1024.f))) {
-          float h = l[0];
-#pragma unroll
-          for (int i = 1; i < V; ++i) h = fmaxf(h, l[i]);
-          m = seg_max<LPR>(h);
-        }
+        if constexpr (GROUPED) m = row_max<S>(l);
+        else m = from_ordered(__reduce_max_sync(FULL_MASK, first));
         const float z = row_softmax<S>(l, m, c);
         inv_z = z > 0.f ? rcp_fast(z) : 0.f;
       }
     }
-    // picks: lane j of the row keeps the j-th (key and lane)
-    uint32_t pick = 0;
-    int from = 0;
-    auto pick_next = [&](int j) {
-      uint32_t top = head[0];
-#pragma unroll
-      for (int cc = 1; cc < C; ++cc) top = max(top, head[cc]);
-      const uint32_t best = seg_max_u32<LPR>(top >> S::IB);
-      const unsigned who = seg_bits<LPR>((top >> S::IB) == best, lane);
-      const int src = __ffs(who) - 1;
-      const uint32_t got = __shfl_sync(FULL_MASK, top, src, LPR);
-      if (q == j) {
-        pick = got;
-        from = src;
-      }
-      if (q == src && got != 0u) {
-        const int cc = C - 1 - static_cast<int>((got & LOW) >> S::IB);
-#pragma unroll
-        for (int u = 0; u < C; ++u)
-          if (C == 1 || u == cc) {
-            uint32_t d = 0u - got;
-#pragma unroll
-            for (int i = 0; i < CE; ++i) d = __viaddmax_u32(key[u * CE + i], 0u - got, d);
-            head[u] = got + d;
-          }
-      }
-    };
-#pragma unroll 1
-    for (int j = 0; j <= k; ++j) pick_next(j);
-    // the picks' values again, the gaps between them
-    int e = 0;
-    bool live = false;
-    float le = -INFINITY, sc = 0.f, val = 0.f, eps = 0.f;
-    auto look_up = [&](int n) {  // lanes q < n
-      const int place = static_cast<int>(LOW) - static_cast<int>(pick & LOW);  // c * CE + i
-      e = ((place / CE) * LPR + from) * CE + place % CE;
-      live = q < n && (pick & ~LOW) > MASKED;
-      if (live) {
-        le = feed.at(x, t, e);
-        if (bias || !cfg.renorm) sc = softmax ? unit_softmax(le, m) * inv_z : sigmoid_fast(le);
-        val = le;
-        eps = 0.f;
-        if constexpr (SCORED) {
-          if (bias) {
-            val = sc + route_smem[e];
-            eps = value_eps(eps_s, softmax, sc, val);
-          }
+    int e = 0x7fffffff;
+    float le = -INFINITY, sc = 0.f, val = -INFINITY, eps = 0.f;
+    if (lane < n) {
+      e = cand[lane].e;
+      le = feed.at(x, t, e);
+      if (masked_logit(le)) le = -INFINITY;  // NaN
+      if (bias || !cfg.renorm) sc = softmax ? (le > -INFINITY ? unit_softmax(le, m) * inv_z : 0.f) : sigmoid_fast(le);
+      val = le;
+      if constexpr (SCORED) {
+        if (bias && le > -INFINITY) {
+          val = sc + route_smem[e];
+          eps = value_eps(eps_s, softmax, sc, val);
         }
-        eps += fabsf(val) * (0x1p-23f * (1u << B)) + 0x1p-126f;
       }
-    };
-    look_up(k + 1);
-    if (!exact_keys) {
-      auto gaps = [&]() {  // bit q: picks q and q + 1 are too near each other
-        const float v2 = __shfl_down_sync(FULL_MASK, val, 1, LPR);
-        const float e2 = __shfl_down_sync(FULL_MASK, eps, 1, LPR);
-        const bool l2 = __shfl_down_sync(FULL_MASK, live ? 1 : 0, 1, LPR) != 0;
-        return seg_bits<LPR>(q + 1 < LPR && l2 && !(val - v2 > eps + e2), lane);
-      };
-      unsigned near = gaps();
-      if (__any_sync(FULL_MASK, near != 0u)) {
-        // more picks, until a gap behind the k-th closes the list
-        int n = k + 1;
-        unsigned ends = (~near >> (k - 1)) & ((1u << (n - k)) - 1u);
-        while (n < LPR && __any_sync(FULL_MASK, near != 0u && ends == 0u)) {
-          pick_next(n);
-          look_up(++n);
-          near = gaps();
-          ends = (~near >> (k - 1)) & ((1u << (n - k)) - 1u);
-        }
-        // the list's experts in the order of their 64-bit values
-        const bool settle = near != 0u && ends != 0u;
-        clear = clear && (near == 0u || ends != 0u);
-        const int len = k - 1 + __ffs(ends);
-        const double z64 = BY == kBySoftmax && bias ? row_z64() : 1.0;
+      cand[lane] = Candidate{val, e, eps, 0};
+    }
+    __syncwarp();
+    int rank = lane < n ? 0 : 32, near = 0;
+    for (int o = 0; o < n; ++o) {
+      const Candidate a = cand[o];
+      rank += a.value > val || (a.value == val && a.e < e);
+      if constexpr (SCORED) near += !(fabsf(a.value - val) > a.eps + eps);
+    }
+    if constexpr (SCORED) {
+      // (a value is near itself; masked ones, -inf, are near each other: so is
+      // what infinities make)
+      if (bias && __any_sync(FULL_MASK, lane < n && near > 1 && val > -INFINITY)) {
+        const double z64 = softmax ? row_z64() : 1.0;
         double v64 = -INFINITY;
-        if (live) {
-          v64 = static_cast<double>(le);
-          if (SCORED && bias) v64 = score_64(le, m, z64, softmax) + static_cast<double>(route_smem[e]);
-        }
-        int rank = 0;
+        if (val > -INFINITY) v64 = score_64(le, m, z64, softmax) + static_cast<double>(route_smem[e]);
+        rank = lane < n ? 0 : 32;
         for (int o = 0; o < n; ++o) {
-          const double ov = __shfl_sync(FULL_MASK, v64, o, LPR);
-          const int oe = __shfl_sync(FULL_MASK, e, o, LPR);
-          rank += o < len && (ov > v64 || (ov == v64 && oe < e));
-        }
-        const int e_old = e;
-        const float l_old = le, s_old = sc;
-        const int live_old = live ? 1 : 0;
-        for (int o = 0; o < n; ++o) {
-          const int r = __shfl_sync(FULL_MASK, rank, o, LPR), oe = __shfl_sync(FULL_MASK, e_old, o, LPR);
-          const float ol = __shfl_sync(FULL_MASK, l_old, o, LPR), os = __shfl_sync(FULL_MASK, s_old, o, LPR);
-          const int ov = __shfl_sync(FULL_MASK, live_old, o, LPR);
-          if (settle && o < len && r == q) {
-            e = oe;
-            le = ol;
-            sc = os;
-            live = ov != 0;
-          }
+          const double ov = __shfl_sync(FULL_MASK, v64, o);
+          const int oe = __shfl_sync(FULL_MASK, e, o);
+          rank += ov > v64 || (ov == v64 && oe < e);
         }
       }
     }
-    const bool mine = q < k && live;
+    const bool mine = rank < k && val > -INFINITY;
     float u = 0.f;
     if (cfg.renorm) {
       const float top = seg_max<LPR>(mine ? le : -INFINITY);
@@ -983,23 +977,22 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
     } else if (mine) {
       u = sc;
     }
-    if (has && clear && q < k) {
-      idx[static_cast<long long>(t) * k + q] = e;
-      gates[static_cast<long long>(t) * k + q] = u * cfg.scale;
-    }
-    unsigned open = __ballot_sync(FULL_MASK, has && !clear && q == 0);
-    while (open) {
-      const int t2 = t0 + (__ffs(open) - 1) / LPR;
-      open &= open - 1;
+    if (clear) {
+      if (rank < k) {
+        idx[static_cast<long long>(t) * k + rank] = e;
+        gates[static_cast<long long>(t) * k + rank] = u * cfg.scale;
+      }
+    } else {
       int e2;
       float g2;
-      route_row_64(x, t2, N, k, cfg, bias, win_s[w], lane, e2, g2);
+      __syncwarp();
+      route_row_64(x, t, N, k, cfg, bias, reinterpret_cast<int*>(cand), lane, e2, g2);
       if (lane < k) {
-        idx[static_cast<long long>(t2) * k + lane] = e2;
-        gates[static_cast<long long>(t2) * k + lane] = g2;
+        idx[static_cast<long long>(t) * k + lane] = e2;
+        gates[static_cast<long long>(t) * k + lane] = g2;
       }
     }
-    if (GROUPED) __syncwarp();  // the group values are read before the next row's are written
+    __syncwarp();  // the candidates and group values are read before the next row's are written
   }
 }
 

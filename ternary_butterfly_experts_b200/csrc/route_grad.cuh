@@ -60,25 +60,6 @@ __device__ __forceinline__ void row_sigmoid(const float (&l)[S::V], float m, boo
     for (int i = 0; i < S::V; ++i) u[i] = masked_logit(l[i]) ? 0.f : exp_fast(l[i] - m) * t[i];
   }
 }
-template <class S>
-__device__ __forceinline__ float row_max(const float (&l)[S::V]) {
-  float h = l[0];
-#pragma unroll
-  for (int i = 1; i < S::V; ++i) h = fmaxf(h, l[i]);
-  return seg_max<S::LPR>(h);
-}
-// Four values of a lane's cell from an array in shared memory.
-template <class S>
-__device__ __forceinline__ void load_cells(const float* a, int q, float (&v)[S::V]) {
-#pragma unroll
-  for (int c = 0; c < S::C; ++c)
-#pragma unroll
-    for (int h = 0; h < S::CE; h += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(a + (c * S::LPR + q) * S::CE + h);
-      v[c * S::CE + h] = f.x, v[c * S::CE + h + 1] = f.y, v[c * S::CE + h + 2] = f.z, v[c * S::CE + h + 3] = f.w;
-    }
-}
-
 // One pass over the logits: the sums of the losses' terms over this block's
 // rows, in a fixed order: part [grid][N] of p_te, zpart [grid] of lse^2, and
 // loads [grid][N + 1], the chosen slots of each expert and the rows.  A lane

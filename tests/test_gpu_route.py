@@ -92,7 +92,7 @@ def test_route_sizes(T, N, k, dtype):
 
 GROUPS = [(40, 256, 8, 8, 4), (33, 64, 2, 4, 2), (21, 24, 5, 3, 2), (19, 60, 4, 5, 1), (50, 250, 8, 10, 3),
           (9, 64, 4, 64, 9), (7, 1024, 8, 16, 2), (11, 4096, 8, 32, 5), (13, 96, 3, 48, 2), (5, 16, 8, 2, 1),
-          (6, 512, 8, 2, 1), (30, 8, 1, 8, 1)]
+          (6, 512, 8, 2, 1), (30, 8, 1, 8, 1), (40, 256, 8, 16, 4), (20, 64, 8, 16, 5), (20, 1024, 8, 64, 3)]
 
 
 @pytest.mark.parametrize("group_score", ["max", "top2"])
