@@ -254,8 +254,12 @@ cudaError_t with_shape(int N, F&& f) {
 template <class S, int BY, bool GROUPED, typename Tl>
 cudaError_t launch_route_rows(Logits<Tl> x, int T, int N, int k, const RouteCfg& cfg, const float* bias, int32_t* idx,
                               float* gates, cudaStream_t s) {
-  int lsh = 0;  // 1 << lsh lanes take a group
+  // 1 << lsh lanes take a group: those that hold it where that is a power of
+  // two, else as many as there are
+  int lsh = 0;
   while (GROUPED && (2 << lsh) * cfg.n_groups <= 32) ++lsh;
+  if (GROUPED && N % (cfg.n_groups * S::CE) == 0 && is_pow2(N / (cfg.n_groups * S::CE)) && S::C == 1)
+    lsh = ilog2(N / (cfg.n_groups * S::CE));
   x.wide = wide_rows<S>(x.p, x.ld, N);
   const size_t floats = (BY != kByLogit ? S::MAXN : 0) + (GROUPED ? kRouteWarps * kGroupSpace<S> : 0) +
                         (x.wide ? kRouteWarps * RowFeed<S, Tl>::BUFFER / 4 : 0);

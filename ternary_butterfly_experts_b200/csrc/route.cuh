@@ -632,6 +632,9 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
     for (int cc = 0; cc < C; ++cc) g0[cc] = (cc * LPR + q) * CE / per;
   }
   const int items = cells ? per / CE : per;  // of a group
+  const bool by_lanes = GROUPED && C == 1 && cells && items == lpg;
+  const bool top2 = cfg.group_score == BFMOE_GROUP_TOP2;
+  const bool fits_64 = cells || kGroupSpace<S> >= 2 * S::MAXN;
 
   const int step = gridDim.x * kRouteWarps;
   int t = blockIdx.x * kRouteWarps + w;
@@ -674,12 +677,117 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
       for (int o = LPR / 2; o > 0; o >>= 1) z += __shfl_xor_sync(FULL_MASK, z, o);
       return z;
     };
+    // The kept groups (bit g) by 64-bit values, for rows whose groups are too
+    // near each other (about 1 in 10^4); by all lanes, needs room for the
+    // values (fits_64).
+    auto groups_64 = [&]() -> unsigned long long {
+      if constexpr (!GROUPED || !SCORED) return 0ull;
+      constexpr int GH = BFMOE_MAX_GROUPS / LPR;
+      const double z64 = softmax ? row_z64() : 1.0;
+      double* gd = reinterpret_cast<double*>(gs);
+      __syncwarp();
+#pragma unroll 1
+      for (int cc = 0; cc < C; ++cc) {
+        double a = -INFINITY, b = -INFINITY;
+#pragma unroll 1
+        for (int i = 0; i < CE; ++i) {
+          const int e = (cc * LPR + q) * CE + i;
+          double v = -INFINITY;
+          if (e < N) {
+            const float le = x.at(t, e);
+            if (!masked_logit(le)) v = score_64(le, m, z64, softmax) + static_cast<double>(route_smem[e]);
+            if (!cells) gd[e] = v;
+          }
+          b = fmax(b, fmin(a, v));
+          a = fmax(a, v);
+        }
+        if (cells) {
+          gd[2 * (cc * LPR + q)] = a;
+          gd[2 * (cc * LPR + q) + 1] = b;
+        }
+      }
+      __syncwarp();
+      // lane q: groups q, q + LPR, ...
+      double gv64[GH];
+      int r64[GH];
+#pragma unroll
+      for (int h = 0; h < GH; ++h) {
+        double a = -INFINITY, b = -INFINITY;
+        const int g = q + h * LPR;
+#pragma unroll 1
+        for (int it = 0; g < cfg.n_groups && it < items; ++it) {
+          const double oa = cells ? gd[2 * (g * items + it)] : gd[g * items + it];
+          const double ob = cells ? gd[2 * (g * items + it) + 1] : -INFINITY;
+          b = fmax(fmin(a, oa), fmax(b, ob));
+          a = fmax(a, oa);
+        }
+        gv64[h] = top2 && b > -INFINITY ? a + b : a;
+        r64[h] = 0;
+      }
+#pragma unroll
+      for (int h = 0; h < GH; ++h)
+#pragma unroll 1
+        for (int o = 0; o < min(cfg.n_groups - h * LPR, LPR); ++o) {
+          const double v = __shfl_sync(FULL_MASK, gv64[h], o, LPR);
+#pragma unroll
+          for (int u = 0; u < GH; ++u)
+            r64[u] += v > gv64[u] || (v == gv64[u] && o + h * LPR < q + u * LPR);
+        }
+      unsigned long long kept64 = 0ull;  // bit g
+#pragma unroll
+      for (int h = 0; h < GH; ++h)
+        kept64 |= static_cast<unsigned long long>(
+                      seg_bits<LPR>(q + h * LPR < cfg.n_groups && r64[h] < cfg.top_groups, lane))
+                  << (h * LPR);
+      return kept64;
+    };
     // groups: the two best of each cell (or every value) go to shared memory,
     // lpg lanes take a group
     bool clear = true;
+    unsigned allowed = V == 32 ? 0xffffffffu : (1u << V) - 1u;
     unsigned long long kept = ~0ull;  // bit g << lsh
-    if constexpr (GROUPED) {
-      const bool top2 = cfg.group_score == BFMOE_GROUP_TOP2;
+    if (GROUPED && by_lanes) {
+      // a group is 1 << lsh neighbouring lanes, each of one cell
+      float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < CE; ++i) {
+        b = fmaxf(b, fminf(a, c[i]));
+        a = fmaxf(a, c[i]);
+      }
+#pragma unroll 1
+      for (int o = 1; o < lpg; o <<= 1) {
+        const float oa = __shfl_xor_sync(FULL_MASK, a, o), ob = __shfl_xor_sync(FULL_MASK, b, o);
+        b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+        a = fmaxf(a, oa);
+      }
+      const float gv = top2 && b > -INFINITY ? a + b : a;
+      int rank = 0;
+#pragma unroll 1
+      for (int o0 = 0; o0 < cfg.n_groups; o0 += lpg) {  // the lanes of a group share the comparisons
+        const int o = o0 + (q & (lpg - 1));
+        const float v = __shfl_sync(FULL_MASK, gv, (o << lsh) & 31);
+        rank += o < cfg.n_groups && (v > gv || (v == gv && o < gq));
+      }
+#pragma unroll 1
+      for (int o = 1; o < lpg; o <<= 1) rank += __shfl_xor_sync(FULL_MASK, rank, o);
+      const bool real = gq < cfg.n_groups;
+      bool in = real && rank < cfg.top_groups;
+      if constexpr (SCORED) {
+        const float worst = -seg_max<LPR>(in ? -gv : -INFINITY), best = seg_max<LPR>(real && !in ? gv : -INFINITY);
+        clear = !(best > -INFINITY) || worst - best > 4.f * value_eps(eps_s, softmax, 1.f, worst);
+        if (!clear) in = (groups_64() >> gq) & 1ull;
+        clear = true;
+        if (!bias) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) c[i] = l[i];
+        }
+      }
+      if (!in) {
+        allowed = 0u;
+#pragma unroll
+        for (int i = 0; i < V; ++i) c[i] = -INFINITY;
+      }
+    } else if constexpr (GROUPED) {
       if (cells) {
 #pragma unroll
         for (int cc = 0; cc < C; ++cc) {
@@ -756,72 +864,10 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
         best = seg_max<LPR>(best);
         // (a sum of two values; a score is at most 1)
         clear = !(best > -INFINITY) || worst - best > 4.f * value_eps(eps_s, softmax, 1.f, worst);
-        // the same in 64 bits for rows whose groups are too near each other
-        // (about 1 in 10^4), where the cells' values fit
-        if ((cells || kGroupSpace<S> >= 2 * S::MAXN) && __any_sync(FULL_MASK, !clear)) {
-          const double z64 = softmax ? row_z64() : 1.0;
-          double* gd = reinterpret_cast<double*>(gs);
-          __syncwarp();
-#pragma unroll 1
-          for (int cc = 0; cc < C; ++cc) {
-            double a = -INFINITY, b = -INFINITY;
-#pragma unroll 1
-            for (int i = 0; i < CE; ++i) {
-              const int e = (cc * LPR + q) * CE + i;
-              double v = -INFINITY;
-              if (e < N) {
-                const float le = x.at(t, e);
-                if (!masked_logit(le)) v = score_64(le, m, z64, softmax) + static_cast<double>(route_smem[e]);
-                if (!cells) gd[e] = v;
-              }
-              b = fmax(b, fmin(a, v));
-              a = fmax(a, v);
-            }
-            if (cells) {
-              gd[2 * (cc * LPR + q)] = a;
-              gd[2 * (cc * LPR + q) + 1] = b;
-            }
-          }
-          __syncwarp();
-          // lane q: groups q, q + LPR, ...
-          double gv64[GH];
-          int r64[GH];
-#pragma unroll
-          for (int h = 0; h < GH; ++h) {
-            double a = -INFINITY, b = -INFINITY;
-            const int g = q + h * LPR;
-#pragma unroll 1
-            for (int it = 0; g < cfg.n_groups && it < items; ++it) {
-              const double oa = cells ? gd[2 * (g * items + it)] : gd[g * items + it];
-              const double ob = cells ? gd[2 * (g * items + it) + 1] : -INFINITY;
-              b = fmax(fmin(a, oa), fmax(b, ob));
-              a = fmax(a, oa);
-            }
-            gv64[h] = top2 && b > -INFINITY ? a + b : a;
-            r64[h] = 0;
-          }
-#pragma unroll
-          for (int h = 0; h < GH; ++h)
-#pragma unroll 1
-            for (int o = 0; o < min(cfg.n_groups - h * LPR, LPR); ++o) {
-              const double v = __shfl_sync(FULL_MASK, gv64[h], o, LPR);
-#pragma unroll
-              for (int u = 0; u < GH; ++u)
-                r64[u] += v > gv64[u] || (v == gv64[u] && o + h * LPR < q + u * LPR);
-            }
-          unsigned long long kept64 = 0ull;  // bit g
-#pragma unroll
-          for (int h = 0; h < GH; ++h)
-            kept64 |= static_cast<unsigned long long>(
-                          seg_bits<LPR>(q + h * LPR < cfg.n_groups && r64[h] < cfg.top_groups, lane))
-                      << (h * LPR);
-          if (!clear) {
-            kept = kept64;
-            if (lsh) {
-              kept = 0ull;
-              for (int g = 0; g < cfg.n_groups; ++g) kept |= ((kept64 >> g) & 1ull) << (g << lsh);
-            }
-          }
+        if (!clear && fits_64) {
+          const unsigned long long kept64 = groups_64();
+          kept = 0ull;
+          for (int g = 0; g < cfg.n_groups; ++g) kept |= ((kept64 >> g) & 1ull) << (g << lsh);
           clear = true;
         }
         if (!bias) {
@@ -831,15 +877,17 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
       }
     }
     // what is no candidate: the other groups, and nothing behind the row's end
-    unsigned allowed = V == 32 ? 0xffffffffu : (1u << V) - 1u;
-    if (GROUPED || N < S::MAXN) {
+    if ((GROUPED && !by_lanes) || N < S::MAXN) {
+      const unsigned before = allowed;
       allowed = 0u;
 #pragma unroll
       for (int cc = 0; cc < C; ++cc) {
         const int e0 = (cc * LPR + q) * CE;
         unsigned in = e0 + CE <= N ? (1u << CE) - 1u : (e0 < N ? (1u << (N - e0)) - 1u : 0u);
         if constexpr (GROUPED) {
-          if (cells) {
+          if (by_lanes) {
+            in &= before;
+          } else if (cells) {
             if (!((kept >> (g0[cc] << lsh)) & 1ull)) in = 0u;
           } else if (in) {
             int g = g0[cc], r = e0 - g * per;
@@ -859,7 +907,7 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
         allowed |= in << (cc * CE);
       }
     }
-    if constexpr (GROUPED) {
+    if (GROUPED && !by_lanes) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (!((allowed >> i) & 1u)) c[i] = -INFINITY;
@@ -947,6 +995,7 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
     }
     __syncwarp();
     int rank = lane < n ? 0 : 32, near = 0;
+#pragma unroll 4
     for (int o = 0; o < n; ++o) {
       const Candidate a = cand[o];
       rank += a.value > val || (a.value == val && a.e < e);
