@@ -30,7 +30,7 @@ using namespace bfmoe;
 namespace {
 
 // Blocks of the loss kernel at most, which leaves one row of partial sums each.
-constexpr int kBalanceBlocks = 320;
+constexpr int kBalanceBlocks = 640;
 
 struct RoutePlan {
   size_t chunk_counts, totals;  // buckets
@@ -241,12 +241,16 @@ int launch_clip(const bfmoe_grad* g, int n, float max_norm, float* norm, double*
   return BFMOE_OK;
 }
 
-// Calls f with the shape that rows of N <= 1024 experts take.
+// Calls f with the shape that rows of N <= 1024 experts take in the gradient
+// and the losses: as few lanes a row as hold it at 16 logits a lane, since what
+// a row takes besides its logits (sums over lanes, the chosen experts) is then
+// shared by 2 or 4 rows of a warp.  65536 x 256 gradients: 38 us with 32 lanes
+// of 8 logits.
 template <class F>
 cudaError_t with_shape(int N, F&& f) {
-  if (N <= 64) return f(RowShape<16, 4>{});
-  if (N <= 128) return f(RowShape<16, 8>{});
-  if (N <= 256) return f(RowShape<32, 8>{});
+  if (N <= 64) return f(RowShape<8, 8>{});
+  if (N <= 128) return f(RowShape<8, 16>{});
+  if (N <= 256) return f(RowShape<16, 16>{});
   if (N <= 512) return f(RowShape<32, 16>{});
   return f(RowShape<32, 32>{});
 }
@@ -262,13 +266,15 @@ cudaError_t launch_route_rows(Logits<Tl> x, int T, int N, int k, const RouteCfg&
     lsh = ilog2(N / (cfg.n_groups * S::CE));
   x.wide = wide_rows<S>(x.p, x.ld, N);
   const size_t floats = (BY != kByLogit ? S::MAXN : 0) + (GROUPED ? kRouteWarps * kGroupSpace<S> : 0) +
-                        (x.wide ? kRouteWarps * RowFeed<S, Tl>::BUFFER / 4 : 0);
-  if (S::V > 8) {
+                        kRouteWarps * RowFeed<S, Tl>::bytes(x.wide) / 4;
+  {
     static std::atomic<uint64_t> done{0};
     if (needs_attr(done)) {
       const cudaError_t e = cudaFuncSetAttribute(route_fast_kernel<S, Tl, BY, GROUPED>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 S::MAXN * 4 + kRouteWarps * (kGroupSpace<S> * 4 + RowFeed<S, Tl>::BUFFER));
+                                                 S::MAXN * 4 + kRouteWarps * (kGroupSpace<S> * 4 +
+                                                                std::max(RowFeed<S, Tl>::bytes(true),
+                                                                         RowFeed<S, Tl>::bytes(false))));
       if (e != cudaSuccess) return e;
       attr_set(done);
     }
@@ -314,7 +320,8 @@ cudaError_t launch_route(const Logits<Tl>& x, int T, int N, int k, const RouteCf
 template <class S, bool SIGMOID, typename Tl>
 cudaError_t launch_balance_rows(Logits<Tl> x, int T, int N, int k, const int32_t* idx, float* part, double* zpart,
                                 int32_t* loads, int* grid, cudaStream_t s) {
-  constexpr size_t most = std::max<size_t>(kGradWarps * S::MAXN * 4, kGradWarps * RowFeed<S, Tl>::BUFFER);
+  constexpr int feed = std::max(RowFeed<S, Tl>::bytes(true), RowFeed<S, Tl>::bytes(false));
+  constexpr size_t most = kGradWarps * std::max(S::MAXN * 4, feed);
   const auto kern = balance_rows_kernel<S, Tl, SIGMOID>;
   static std::atomic<uint64_t> done{0};
   if (needs_attr(done)) {
@@ -325,7 +332,7 @@ cudaError_t launch_balance_rows(Logits<Tl> x, int T, int N, int k, const int32_t
   x.wide = wide_rows<S>(x.p, x.ld, N);
   // a warp takes several rows where there are enough, so that the sums that
   // are left to add up stay few
-  *grid = grid_for(T, kGradWarps * S::ROWS * 2, std::min(kBalanceBlocks, sm_count() * 2));
+  *grid = grid_for(T, kGradWarps * S::ROWS * 2, std::min(kBalanceBlocks, sm_count() * kBalanceRowBlocks<S>));
   return launch("balance_rows", s, [&] {
     pdl_launch(kern, *grid, kGradWarps * 32, most, s, x, T, N, k, idx, part, zpart, loads);
   });
@@ -354,10 +361,11 @@ cudaError_t launch_balance(const Logits<Tl>& x, int T, int N, int k, bool sigmoi
   });
 }
 
-template <class S, bool SIGMOID, typename Tl>
+template <class S, bool SIGMOID, bool ROW, typename Tl>
 cudaError_t launch_backward_rows(Logits<Tl> x, int T, int N, int k, const RouteCfg& cfg, RouteGrad g, cudaStream_t s) {
-  constexpr size_t base = S::MAXN * (1 + kGradWarps * S::ROWS) * 4, most = base + kGradWarps * RowFeed<S, Tl>::BUFFER;
-  const auto kern = route_backward_kernel<S, Tl, SIGMOID>;
+  constexpr size_t base = S::MAXN * (1 + kGradWarps * S::ROWS) * 4;
+  constexpr size_t most = base + kGradWarps * std::max(RowFeed<S, Tl>::bytes(true), RowFeed<S, Tl>::bytes(false));
+  const auto kern = route_backward_kernel<S, Tl, SIGMOID, ROW>;
   static std::atomic<uint64_t> done{0};
   if (needs_attr(done)) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
@@ -366,9 +374,9 @@ cudaError_t launch_backward_rows(Logits<Tl> x, int T, int N, int k, const RouteC
   }
   x.wide = wide_rows<S>(x.p, x.ld, N);
   g.wide_out = wide_rows<S>(static_cast<const Tl*>(g.out), g.ld_out, N);
-  const int grid = grid_for(T, kGradWarps * S::ROWS, sm_count() * kGradRowBlocks<S>);
+  const int grid = grid_for(T, kGradWarps * S::ROWS, sm_count() * (ROW ? kGradRowBlocks<S> : 4));
   return launch("route_backward", s, [&] {
-    pdl_launch(kern, grid, kGradWarps * 32, x.wide ? most : base, s, x, T, N, k, cfg, g);
+    pdl_launch(kern, grid, kGradWarps * 32, base + (ROW ? kGradWarps * RowFeed<S, Tl>::bytes(x.wide) : 0), s, x, T, N, k, cfg, g);
   });
 }
 
@@ -378,8 +386,14 @@ cudaError_t launch_route_backward(const Logits<Tl>& x, int T, int N, int k, cons
   if (N <= 1024)
     return with_shape(N, [&](auto shape) {
       using S = decltype(shape);
-      if (cfg.score == BFMOE_SCORE_SIGMOID) return launch_backward_rows<S, true>(x, T, N, k, cfg, g, s);
-      return launch_backward_rows<S, false>(x, T, N, k, cfg, g, s);
+      const bool sigmoid = cfg.score == BFMOE_SCORE_SIGMOID;
+      // losses, and gates that are a softmax of the whole row, reach every logit
+      if (!g.load && (sigmoid || cfg.renorm)) {
+        if (sigmoid) return launch_backward_rows<S, true, false>(x, T, N, k, cfg, g, s);
+        return launch_backward_rows<S, false, false>(x, T, N, k, cfg, g, s);
+      }
+      if (sigmoid) return launch_backward_rows<S, true, true>(x, T, N, k, cfg, g, s);
+      return launch_backward_rows<S, false, true>(x, T, N, k, cfg, g, s);
     });
   return launch("route_backward", s, [&] {
     pdl_launch(route_backward_long_kernel<Tl>, grid_for(T, kGradWarps, sm_count() * 8), kGradWarps * 32, 0, s, x, T, N, k,

@@ -86,7 +86,7 @@ struct Logits {
   static constexpr bool BF16 = sizeof(T) == 2;
   const T* p;
   long long ld;
-  int wide;  // rows are whole cells of 16-byte aligned memory (RowShape)
+  int wide;  // rows are whole cells of memory aligned to cells (RowShape)
   __device__ __forceinline__ float at(int t, int e) const { return to_f32(p[static_cast<long long>(t) * ld + e]); }
 };
 
@@ -357,19 +357,69 @@ struct RowShape {
   static_assert(CE >= 2 && C <= 4);
 };
 
+// Where expert e's float32 lies in an array in shared memory that lanes read in
+// cells: the halves of eight-expert cells apart, so that the 16 bytes of
+// neighbouring lanes follow each other (32 apart, every read took two passes).
+template <class S>
+__device__ __forceinline__ int slot_of(int e) {
+  if constexpr (S::CE < 8) return e;
+  const int cell = e >> 3;
+  return ((cell / S::LPR * 2 + ((e >> 2) & 1)) * S::LPR + cell % S::LPR) * 4 + (e & 3);
+}
+// A lane's cells of such an array.
+template <class S>
+__device__ __forceinline__ void load_cells(const float* a, int q, float (&v)[S::V]) {
+  if constexpr (S::CE == 2) {
+    const float2 f = *reinterpret_cast<const float2*>(a + q * 2);
+    v[0] = f.x, v[1] = f.y;
+  } else {
+#pragma unroll
+    for (int h = 0; h < S::V; h += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(a + (h / 4 * S::LPR + q) * 4);
+      v[h] = f.x, v[h + 1] = f.y, v[h + 2] = f.z, v[h + 3] = f.w;
+    }
+  }
+}
+
+// Cell c of them, read and written.
+template <class S>
+__device__ __forceinline__ void load_cell_of(const float* a, int q, int c, float (&v)[S::CE]) {
+#pragma unroll
+  for (int h = 0; h < S::CE; h += 4) {
+    const float4 f = *reinterpret_cast<const float4*>(a + ((c * S::CE + h) / 4 * S::LPR + q) * 4);
+    v[h] = f.x, v[h + 1] = f.y, v[h + 2] = f.z, v[h + 3] = f.w;
+  }
+}
+template <class S>
+__device__ __forceinline__ void store_cell_of(float* a, int q, int c, const float (&v)[S::CE]) {
+#pragma unroll
+  for (int h = 0; h < S::CE; h += 4)
+    *reinterpret_cast<float4*>(a + ((c * S::CE + h) / 4 * S::LPR + q) * 4) = make_float4(v[h], v[h + 1], v[h + 2], v[h + 3]);
+}
+
 // A row's words as they are in memory, so that the next row can be on its way
 // while one is worked on.  Words behind the row's end are -inf of its type.
 template <class S, typename Tl>
 struct RawRow {
   static constexpr bool BF16 = sizeof(Tl) == 2;
-  static constexpr int W = BF16 ? S::V / 2 : S::V;  // words
-  static constexpr int CW = W / S::C;               // of a cell: 1, 2, 4 or 8
-  uint32_t w[W];
+  static constexpr int CW = S::CE * static_cast<int>(sizeof(Tl)) / 4;  // words of a cell: 1, 2, 4 or 8
+  uint32_t w[S::V];
 
-  // A cell from aligned memory (to 16 bytes, or a smaller cell), global or
-  // shared.
+  // A cell from aligned memory (to its size), global or shared.
+  template <bool GLOBAL>
   __device__ __forceinline__ void load_cell(int c, const Tl* p, bool in) {
     constexpr uint32_t M = BF16 ? 0xff80ff80u : 0xff800000u;
+    if constexpr (CW == 8 && GLOBAL) {
+      uint32_t* v = w + 8 * c;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = M;
+      if (in)
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                     : "l"(p)
+                     : "memory");
+      return;
+    }
     if constexpr (CW == 1) {
       w[c] = in ? *reinterpret_cast<const uint32_t*>(p) : M;
     } else if constexpr (CW == 2) {
@@ -390,25 +440,14 @@ struct RawRow {
 #pragma unroll
       for (int c = 0; c < S::C; ++c) {
         const int e0 = (c * S::LPR + q) * S::CE;
-        load_cell(c, row + e0, e0 < N);
+        load_cell<true>(c, row + e0, e0 < N);
       }
-    } else {
+    } else {  // logit i is that of expert i LPR + q
 #pragma unroll
-      for (int c = 0; c < S::C; ++c) {
-        const int e0 = (c * S::LPR + q) * S::CE;
-        if constexpr (BF16) {
-          const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
-#pragma unroll
-          for (int h = 0; h < CW; ++h) {
-            const int e = e0 + 2 * h;
-            const uint32_t a = e < N ? p[e] : 0xff80u, b = e + 1 < N ? p[e + 1] : 0xff80u;
-            w[CW * c + h] = a | b << 16;
-          }
-        } else {
-          const uint32_t* p = reinterpret_cast<const uint32_t*>(row);
-#pragma unroll
-          for (int h = 0; h < CW; ++h) w[CW * c + h] = e0 + h < N ? p[e0 + h] : 0xff800000u;
-        }
+      for (int i = 0; i < S::V; ++i) {
+        const int e = i * S::LPR + q;
+        if constexpr (BF16) w[i] = e < N ? reinterpret_cast<const uint16_t*>(row)[e] : 0xff80u;
+        else w[i] = e < N ? reinterpret_cast<const uint32_t*>(row)[e] : 0xff800000u;
       }
     }
   }
@@ -416,26 +455,32 @@ struct RawRow {
   __device__ __forceinline__ void load_shared(const uint8_t* row, int q) {
 #pragma unroll
     for (int c = 0; c < S::C; ++c)
-      load_cell(c, reinterpret_cast<const Tl*>(row) + (c * S::LPR + q) * S::CE, true);
+      load_cell<false>(c, reinterpret_cast<const Tl*>(row) + (c * S::LPR + q) * S::CE, true);
   }
   // The logits, NaN as -inf; of bfloat16, whose equal values meet as keys, -0
   // as 0.
-  __device__ __forceinline__ void unpack(float (&l)[S::V]) const {
+  __device__ __forceinline__ void unpack(bool wide, float (&l)[S::V]) const {
+    if constexpr (BF16) {
+      if (wide) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      if constexpr (BF16) {
-        l[2 * i] = fmaxf(__uint_as_float(w[i] << 16), -INFINITY) + 0.f;
-        l[2 * i + 1] = fmaxf(__uint_as_float(w[i] & 0xffff0000u), -INFINITY) + 0.f;
+        for (int i = 0; i < S::V / 2; ++i) {
+          l[2 * i] = fmaxf(__uint_as_float(w[i] << 16), -INFINITY) + 0.f;
+          l[2 * i + 1] = fmaxf(__uint_as_float(w[i] & 0xffff0000u), -INFINITY) + 0.f;
+        }
       } else {
-        l[i] = fmaxf(__uint_as_float(w[i]), -INFINITY);
+#pragma unroll
+        for (int i = 0; i < S::V; ++i) l[i] = fmaxf(__uint_as_float(w[i] << 16), -INFINITY) + 0.f;
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < S::V; ++i) l[i] = fmaxf(__uint_as_float(w[i]), -INFINITY);
     }
   }
 };
 // Whether rows can be read in cells (Logits::wide).
 template <class S, typename Tl>
 inline bool wide_rows(const Tl* p, long long ld, int N) {
-  const size_t bytes = std::min<size_t>(16, S::CE * sizeof(Tl));
+  const size_t bytes = S::CE * sizeof(Tl);
   return N % S::CE == 0 && ld % S::CE == 0 && reinterpret_cast<uintptr_t>(p) % bytes == 0;
 }
 
@@ -454,7 +499,10 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 template <class S, typename Tl>
 struct RowFeed {
   static constexpr bool AHEAD = S::V <= 8;
-  static constexpr int BUFFER = AHEAD ? 0 : 2 * S::MAXN * static_cast<int>(sizeof(Tl));  // bytes of shared memory of a warp
+  static constexpr int ROW = S::MAXN * static_cast<int>(sizeof(Tl));
+  // Bytes of shared memory of a warp: rows in cells go through two buffers (not
+  // AHEAD), others are brought into cells through one in float32.
+  __host__ __device__ static constexpr int bytes(bool wide) { return wide ? (AHEAD ? 0 : 2 * S::ROWS * ROW) : S::ROWS * S::MAXN * 4; }
   RawRow<S, Tl> raw;
   uint8_t* buf;
   uint64_t* full;
@@ -462,10 +510,12 @@ struct RowFeed {
   int turn;
   bool staged;
 
-  __device__ __forceinline__ void fetch(const Logits<Tl>& x, int t, int N, int b) {  // one lane
-    const int bytes = N * static_cast<int>(sizeof(Tl));
-    mbar_expect_tx(full + b, bytes);
-    bulk_load(buf + b * (BUFFER / 2), x.p + static_cast<long long>(t) * x.ld, bytes, full + b);
+  // one lane: the rows from t on into buffer b
+  __device__ __forceinline__ void fetch(const Logits<Tl>& x, int t, int T, int N, int b) {
+    const int bytes = N * static_cast<int>(sizeof(Tl)), rows = min(S::ROWS, T - t);
+    mbar_expect_tx(full + b, rows * bytes);
+    for (int r = 0; r < rows; ++r)
+      bulk_load(buf + (b * S::ROWS + r) * ROW, x.p + static_cast<long long>(t + r) * x.ld, bytes, full + b);
   }
   // bars: two of the warp's (not AHEAD)
   __device__ __forceinline__ void start(const Logits<Tl>& x, int t0, int T, int N, int lane, uint8_t* buffer, uint64_t* bars) {
@@ -479,43 +529,62 @@ struct RowFeed {
     } else if (staged) {
       // behind the row's end the buffers hold -inf, which no copy reaches
       for (int e = N + lane; e < S::MAXN; e += 32)
-        for (int b = 0; b < 2; ++b) reinterpret_cast<Tl*>(buf + b * (BUFFER / 2))[e] = from_f32<Tl>(-INFINITY);
+        for (int b = 0; b < 2 * S::ROWS; ++b) reinterpret_cast<Tl*>(buf + b * ROW)[e] = from_f32<Tl>(-INFINITY);
       if (lane == 0) {
         mbar_init(full, 1);
         mbar_init(full + 1, 1);
         mbar_fence_init();
-        if (t0 < T) fetch(x, t0, N, 0);
+        if (t0 < T) fetch(x, t0, T, N, 0);
       }
       __syncwarp();
     }
   }
-  // The logits of the warp's rows at t0 (a row past the end: the last one's).
+  // The logits of the warp's rows at t0 (past the end: anything).
   // False after a copy that did not come, which is reported: then nothing of
   // the warp's is on its way any more.
   __device__ __forceinline__ bool take(const Logits<Tl>& x, int t0, int step, int T, int N, int lane, float (&l)[S::V]) {
     const int q = lane & (S::LPR - 1);
     if constexpr (AHEAD) {
-      raw.unpack(l);
+      raw.unpack(x.wide, l);
       if (t0 + step < T) raw.load(x, min(t0 + step + lane / S::LPR, T - 1), N, q);
     } else {
       if (staged) {
         const int b = turn & 1;
         // the buffer of the row before was read before that row's work
-        if (lane == 0 && t0 + step < T) fetch(x, t0 + step, N, b ^ 1);
+        if (lane == 0 && t0 + step < T) fetch(x, t0 + step, T, N, b ^ 1);
         if (__any_sync(FULL_MASK, !mbar_wait(full + b, (turn >> 1) & 1, 0x2100u))) {
           if (t0 + step < T) mbar_wait(full + (b ^ 1), ((turn + 1) >> 1) & 1, 0x2101u);
           return false;
         }
-        here = buf + b * (BUFFER / 2);
+        here = buf + (b * S::ROWS + lane / S::LPR) * ROW;
         raw.load_shared(here, q);
         __syncwarp();
         ++turn;
       } else {
         raw.load(x, min(t0 + lane / S::LPR, T - 1), N, q);
       }
-      raw.unpack(l);
+      raw.unpack(x.wide, l);
+    }
+    if (!x.wide) {
+      float* cells = reinterpret_cast<float*>(buf) + lane / S::LPR * S::MAXN;
+#pragma unroll
+      for (int i = 0; i < S::V; ++i) cells[slot_of<S>(i * S::LPR + q)] = l[i];
+      __syncwarp();
+      load_cells<S>(cells, q, l);
+      __syncwarp();
     }
     return true;
+  }
+  // The row taken last once more (rows of registers are there still).
+  __device__ __forceinline__ void again(const Logits<Tl>& x, int t, int N, int lane, float (&l)[S::V]) {
+    if constexpr (!AHEAD) {
+      if (here) {
+        raw.load_shared(here, lane & (S::LPR - 1));
+        raw.unpack(x.wide, l);
+      } else {
+        load_cells<S>(reinterpret_cast<const float*>(buf) + lane / S::LPR * S::MAXN, lane & (S::LPR - 1), l);
+      }
+    }
   }
   // Logit e of row t, the row taken last.
   __device__ __forceinline__ float at(const Logits<Tl>& x, int t, int e) const {
@@ -547,23 +616,6 @@ __device__ __forceinline__ float row_max(const float (&l)[S::V]) {
   for (int i = 1; i < S::V; ++i) h = fmaxf(h, l[i]);
   return seg_max<S::LPR>(h);
 }
-// A lane's cells from an array in shared memory.
-template <class S>
-__device__ __forceinline__ void load_cells(const float* a, int q, float (&v)[S::V]) {
-  if constexpr (S::CE == 2) {
-    const float2 f = *reinterpret_cast<const float2*>(a + q * 2);
-    v[0] = f.x, v[1] = f.y;
-  } else {
-#pragma unroll
-    for (int c = 0; c < S::C; ++c)
-#pragma unroll
-      for (int h = 0; h < S::CE; h += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(a + (c * S::LPR + q) * S::CE + h);
-        v[c * S::CE + h] = f.x, v[c * S::CE + h + 1] = f.y, v[c * S::CE + h + 2] = f.z, v[c * S::CE + h + 3] = f.w;
-      }
-  }
-}
-
 // What ranks the experts: the logits, or softmax or sigmoid scores (with a
 // bias, or summed up by group).
 enum { kByLogit = 0, kBySoftmax = 1, kBySigmoid = 2 };
@@ -619,7 +671,7 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
   pdl_trigger();
   if constexpr (SCORED) {
     for (int e = threadIdx.x; e < S::MAXN; e += blockDim.x)
-      route_smem[e] = bias && e < N ? fmaxf(bias[e], -INFINITY) : 0.f;  // NaN masks
+      route_smem[slot_of<S>(e)] = bias && e < N ? fmaxf(bias[e], -INFINITY) : 0.f;  // NaN masks
     __syncthreads();
   }
   const float eps_s = score_eps(softmax, V);
@@ -642,7 +694,7 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
   RowFeed<S, Tl> feed;
   feed.start(x, t, T, N, lane,
              reinterpret_cast<uint8_t*>(route_smem + (SCORED ? S::MAXN : 0) + (GROUPED ? kRouteWarps * kGroupSpace<S> : 0)) +
-                 static_cast<size_t>(w) * RowFeed<S, Tl>::BUFFER,
+                 w * RowFeed<S, Tl>::bytes(x.wide),
              full_s + w * 2);
   for (; t < T; t += step) {
     float l[V], c[V];
@@ -695,7 +747,7 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
           double v = -INFINITY;
           if (e < N) {
             const float le = x.at(t, e);
-            if (!masked_logit(le)) v = score_64(le, m, z64, softmax) + static_cast<double>(route_smem[e]);
+            if (!masked_logit(le)) v = score_64(le, m, z64, softmax) + static_cast<double>(route_smem[slot_of<S>(e)]);
             if (!cells) gd[e] = v;
           }
           b = fmax(b, fmin(a, v));
@@ -987,7 +1039,7 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
       val = le;
       if constexpr (SCORED) {
         if (bias && le > -INFINITY) {
-          val = sc + route_smem[e];
+          val = sc + route_smem[slot_of<S>(e)];
           eps = value_eps(eps_s, softmax, sc, val);
         }
       }
@@ -1007,7 +1059,7 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
       if (bias && __any_sync(FULL_MASK, lane < n && near > 1 && val > -INFINITY)) {
         const double z64 = softmax ? row_z64() : 1.0;
         double v64 = -INFINITY;
-        if (val > -INFINITY) v64 = score_64(le, m, z64, softmax) + static_cast<double>(route_smem[e]);
+        if (val > -INFINITY) v64 = score_64(le, m, z64, softmax) + static_cast<double>(route_smem[slot_of<S>(e)]);
         rank = lane < n ? 0 : 32;
         for (int o = 0; o < n; ++o) {
           const double ov = __shfl_sync(FULL_MASK, v64, o);

@@ -18,7 +18,9 @@ namespace bfmoe {
 
 constexpr int kGradWarps = 8;
 template <class S>
-constexpr int kGradRowBlocks = S::V <= 8 ? 4 : 2;  // of an SM
+constexpr int kGradRowBlocks = S::V <= 8 ? 4 : (S::V <= 16 ? 3 : 2);  // of an SM
+template <class S>
+constexpr int kBalanceRowBlocks = S::V <= 8 ? 4 : (S::V <= 16 ? 3 : 2);
 
 // lse of a row from its largest logit and sum of exp(l - m).
 __device__ __forceinline__ float row_lse(float m, float z) { return m + __logf(z); }
@@ -36,10 +38,11 @@ struct TwoSided {
 // sigmoid(-l) in t; masked logits give 0 and 1.  Where softmax terms x =
 // exp(l - m) are at hand and the largest logit is moderate, sigmoid(l) is
 // x / (x + exp(-m)): no second exponential.
+__device__ __forceinline__ bool moderate(float m) { return !__any_sync(FULL_MASK, !(m >= -10.f && m <= 40.f)); }
 template <class S>
 __device__ __forceinline__ void row_sigmoid(const float (&l)[S::V], float m, bool has_x, const float (&x)[S::V],
                                             float (&u)[S::V], float (&t)[S::V]) {
-  if (has_x && !__any_sync(FULL_MASK, !(m >= -10.f && m <= 40.f))) {
+  if (has_x && moderate(m)) {
     const float c = exp_fast(-m);
 #pragma unroll
     for (int i = 0; i < S::V; ++i) {
@@ -65,7 +68,7 @@ __device__ __forceinline__ void row_sigmoid(const float (&l)[S::V], float m, boo
 // loads [grid][N + 1], the chosen slots of each expert and the rows.  A lane
 // keeps the sums of its experts in registers.
 template <class S, typename Tl, bool SIGMOID>
-__global__ __launch_bounds__(kGradWarps * 32, kGradRowBlocks<S>) void balance_rows_kernel(
+__global__ __launch_bounds__(kGradWarps * 32, kBalanceRowBlocks<S>) void balance_rows_kernel(
     const Logits<Tl> x, int T, int N, int k, const int32_t* __restrict__ idx, float* __restrict__ part,
     double* __restrict__ zpart, int32_t* __restrict__ loads) {
   constexpr int LPR = S::LPR, V = S::V;
@@ -87,7 +90,7 @@ __global__ __launch_bounds__(kGradWarps * 32, kGradRowBlocks<S>) void balance_ro
   const int step = gridDim.x * kGradWarps * S::ROWS;
   int t0 = (blockIdx.x * kGradWarps + w) * S::ROWS;
   RowFeed<S, Tl> feed;
-  feed.start(x, t0, T, N, lane, reinterpret_cast<uint8_t*>(grad_smem) + static_cast<size_t>(w) * RowFeed<S, Tl>::BUFFER,
+  feed.start(x, t0, T, N, lane, reinterpret_cast<uint8_t*>(grad_smem) + w * RowFeed<S, Tl>::bytes(x.wide),
              full_s + w * 2);
   auto slot = [&](int t) { return q < k && t < T ? idx[static_cast<long long>(t) * k + q] : -1; };
   int e = slot(t0 + lane / LPR);
@@ -102,8 +105,15 @@ __global__ __launch_bounds__(kGradWarps * 32, kGradRowBlocks<S>) void balance_ro
     const float z = row_softmax<S>(l, m, u);
     float inv;
     if constexpr (SIGMOID) {
-      float c[V];
-      row_sigmoid<S>(l, m, true, u, u, c);
+      if (moderate(m)) {
+        const float c = exp_fast(-m);
+#pragma unroll
+        for (int i = 0; i < V; ++i) u[i] *= rcp_fast(u[i] + c);
+      } else {
+        float c[V];
+        feed.again(x, min(t, T - 1), N, lane, l);
+        row_sigmoid<S>(l, m, false, u, u, c);
+      }
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) s += u[i];
@@ -326,11 +336,17 @@ __global__ __cluster_dims__(kFinishBlocks, 1, 1) __launch_bounds__(kFinishThread
   }
 }
 
-// CE consecutive float32 values to an aligned cell.
+// CE consecutive float32 values to an aligned cell.  (Eight in one store: as
+// two, each wrote half of every 32-byte sector that it touched.)
 template <int CE>
 __device__ __forceinline__ void store_cell(float* p, const float* v) {
-#pragma unroll
-  for (int h = 0; h < CE; h += 4) *reinterpret_cast<float4*>(p + h) = make_float4(v[h], v[h + 1], v[h + 2], v[h + 3]);
+  if constexpr (CE == 8) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  }
 }
 template <int CE>
 __device__ __forceinline__ void store_cell(__nv_bfloat16* p, const float* v) {
@@ -372,9 +388,9 @@ struct LossFactors {
 // A row in registers: the gradient of every logit is p_e (a_e + K) from the
 // losses and the plain softmax's gates (a_e = cb load_e, K the row's sums), and
 // each chosen expert has its own term, which reaches its lane through shared
-// memory.  Where only chosen experts have one, the row is not read.
-template <class S, typename Tl, bool SIGMOID>
-__global__ __launch_bounds__(kGradWarps * 32, kGradRowBlocks<S>) void route_backward_kernel(const Logits<Tl> x, int T, int N,
+// memory.  Where only chosen experts have one (ROW false), the row is not read.
+template <class S, typename Tl, bool SIGMOID, bool ROW>
+__global__ __launch_bounds__(kGradWarps * 32, ROW ? kGradRowBlocks<S> : 4) void route_backward_kernel(const Logits<Tl> x, int T, int N,
                                                                                             int k, const RouteCfg cfg,
                                                                                             const RouteGrad g) {
   constexpr int LPR = S::LPR, V = S::V;
@@ -388,40 +404,53 @@ __global__ __launch_bounds__(kGradWarps * 32, kGradRowBlocks<S>) void route_back
   pdl_trigger();
   const LossFactors f(g, N, k);
   for (int e = threadIdx.x; e < S::MAXN; e += blockDim.x)
-    grad_smem[e] = e < N && f.cb != 0.f ? f.cb * static_cast<float>(g.load[e]) : 0.f;
+    grad_smem[slot_of<S>(e)] = e < N && f.cb != 0.f ? f.cb * static_cast<float>(g.load[e]) : 0.f;
   __syncthreads();
   const bool dense = g.dgates && !SIGMOID && !cfg.renorm;  // every logit moves every gate
-  const bool need_row = dense || f.cb != 0.f || f.cz != 0.f;
   const int step = gridDim.x * kGradWarps * S::ROWS;
   int t0 = (blockIdx.x * kGradWarps + w) * S::ROWS;
   RowFeed<S, Tl> feed;
-  if (need_row)
+  if constexpr (ROW)
     feed.start(x, t0, T, N, lane,
                reinterpret_cast<uint8_t*>(grad_smem + S::MAXN * (1 + kGradWarps * S::ROWS)) +
-                   static_cast<size_t>(w) * RowFeed<S, Tl>::BUFFER,
+                   w * RowFeed<S, Tl>::bytes(x.wide),
                full_s + w * 2);
-  else
-    feed.here = nullptr;
-  int e_next = -1;
-  float dg_next = 0.f;
-  auto slot = [&](int t) {
-    e_next = -1;
-    dg_next = 0.f;
+  // lane q < k holds slot q of its row.  Loads run ahead: a row's experts and
+  // gate gradients by two rows, and, where the row itself is not read, the
+  // logits of its experts by one.  (Nothing is computed from what was just
+  // loaded: that would wait for it.)
+  struct Slot {
+    int e;
+    float dg, l;
+  } now{-1, 0.f, -INFINITY}, next{-1, 0.f, -INFINITY}, after{-1, 0.f, -INFINITY};
+  auto ask = [&](Slot& s, int t) {
+    s.e = -1;
     if (g.dgates && q < k && t < T) {
-      e_next = g.idx[static_cast<long long>(t) * k + q];
-      dg_next = g.dgates[static_cast<long long>(t) * k + q] * cfg.scale;
+      s.e = g.idx[static_cast<long long>(t) * k + q];
+      s.dg = g.dgates[static_cast<long long>(t) * k + q];
     }
   };
-  slot(t0 + lane / LPR);
+  auto ask_logit = [&](Slot& s, int t) {
+    s.l = -INFINITY;
+    if (!ROW && s.e >= 0 && s.e < N) s.l = x.at(t, s.e);
+  };
+  ask(next, t0 + lane / LPR);
+  ask(after, t0 + step + lane / LPR);
+  ask_logit(next, t0 + lane / LPR);
   for (; t0 < T; t0 += step) {
     const int t = min(t0 + lane / LPR, T - 1);
     const bool has = t0 + lane / LPR < T;
-    float l[V], u[V], tt[V], a[V];
-    if (need_row && !feed.take(x, t0, step, T, N, lane, l)) return;
-    int e = e_next;
-    const float dg = dg_next;
-    slot(t0 + step + lane / LPR);
-    // the chosen: lane q < k holds slot q
+    float l[ROW ? V : 1], u[ROW ? V : 1], tt[ROW && SIGMOID ? V : 1];
+    if constexpr (ROW) {
+      if (!feed.take(x, t0, step, T, N, lane, l)) return;
+    }
+    now = next;
+    next = after;
+    ask_logit(next, t0 + step + lane / LPR);
+    ask(after, t0 + 2 * step + lane / LPR);
+    int e = now.e;
+    const float dg = now.dg * cfg.scale;
+    // the chosen
     float le = -INFINITY;
     bool live = false;
     if (g.dgates) {
@@ -429,13 +458,15 @@ __global__ __launch_bounds__(kGradWarps * 32, kGradRowBlocks<S>) void route_back
         report_error(BFMOE_EDEVICE_BOUNDS, static_cast<unsigned>(t));
         e = -1;
       }
-      if (e >= 0) le = feed.at(x, t, e);
+      if (e >= 0) {
+        if constexpr (ROW) le = feed.at(x, t, e);
+        else le = now.l;
+      }
       live = e >= 0 && !masked_logit(le);
     }
     float m = 0.f, inv = 0.f, pa = 0.f, lse = 0.f;
-    if (need_row) {
+    if constexpr (ROW) {
       m = row_max<S>(l);
-      load_cells<S>(grad_smem, q, a);
       float s = 0.f;
       if constexpr (SIGMOID) {
         if (f.cz != 0.f) {  // softmax_e lse cz is added at the end
@@ -454,7 +485,12 @@ __global__ __launch_bounds__(kGradWarps * 32, kGradRowBlocks<S>) void route_back
       if (f.cb != 0.f) {
         float b = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) b = fmaf(u[i], a[i], b);
+        for (int c = 0; c < S::C; ++c) {
+          float a[S::CE];
+          load_cell_of<S>(grad_smem, q, c, a);
+#pragma unroll
+          for (int i = 0; i < S::CE; ++i) b = fmaf(u[c * S::CE + i], a[i], b);
+        }
         pa = seg_sum<LPR>(b) * inv;
       }
     }
@@ -474,73 +510,62 @@ __global__ __launch_bounds__(kGradWarps * 32, kGradRowBlocks<S>) void route_back
       }
       if (SIGMOID) d = live ? d * sigmoid_fast(-le) : 0.f;
       // the terms of one expert chosen twice add up in slot order
-      const unsigned same = __match_any_sync(FULL_MASK, e >= 0 ? (lane & ~(LPR - 1)) * BFMOE_MAX_EXPERTS + e : ~lane);
-      if (__any_sync(FULL_MASK, (same & (same - 1)) != 0u)) {
-        float all = 0.f;
-        for (int o = 0; o < k; ++o) {
-          const float v = __shfl_sync(FULL_MASK, d, o, LPR);
-          if ((same >> ((lane & ~(LPR - 1)) + o)) & 1u) all += v;
-        }
-        d = all;
+      float all = 0.f;
+      for (int o = 0; o < k; ++o) {
+        const int eo = __shfl_sync(FULL_MASK, e, o, LPR);
+        const float v = __shfl_sync(FULL_MASK, d, o, LPR);
+        all += eo == e ? v : 0.f;
       }
-      if (e >= 0) mine[e] = d;
+      d = all;
+      if (e >= 0) mine[slot_of<S>(e)] = d;
       __syncwarp();
-    }
-    float o[V];
-    if (g.dgates) {
-      load_cells<S>(mine, q, o);
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) o[i] = 0.f;
-    }
-    if (need_row) {
-      if constexpr (SIGMOID) {
-        if (f.cb != 0.f) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) o[i] = fmaf(u[i] * inv * tt[i], a[i] - pa, o[i]);
-        }
-        if (f.cz != 0.f) {
-          row_softmax<S>(l, m, u);
-#pragma unroll
-          for (int i = 0; i < V; ++i) o[i] = fmaf(u[i], lse, o[i]);
-        }
-      } else {
-        const float K = lse - pa - dot;
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = fmaf(u[i] * inv, a[i] + K, o[i]);
-      }
     }
     Tl* row_out = static_cast<Tl*>(g.out) + static_cast<long long>(t) * g.ld_out;
-    if (g.wide_out) {
-      if (has) {
+    const float K = lse - pa - dot;  // (softmax)
 #pragma unroll
-        for (int c = 0; c < S::C; ++c) {
-          const int e0 = (c * LPR + q) * S::CE;
-          if (e0 < N) store_cell<S::CE>(row_out + e0, o + c * S::CE);
+    for (int c = 0; c < S::C; ++c) {
+      float o[S::CE];
+      if (g.dgates) {
+        load_cell_of<S>(mine, q, c, o);
+      } else {
+#pragma unroll
+        for (int i = 0; i < S::CE; ++i) o[i] = 0.f;
+      }
+      if constexpr (ROW) {
+        float a[S::CE];
+        load_cell_of<S>(grad_smem, q, c, a);
+#pragma unroll
+        for (int i = 0; i < S::CE; ++i) {
+          const int v = c * S::CE + i;
+          if constexpr (SIGMOID) {
+            o[i] = fmaf(u[v] * inv * tt[v], a[i] - pa, o[i]);
+            if (f.cz != 0.f && !masked_logit(l[v])) o[i] = fmaf(unit_softmax(l[v], m), lse, o[i]);
+          } else {
+            o[i] = fmaf(u[v] * inv, a[i] + K, o[i]);
+          }
         }
       }
-    } else {
+      const int e0 = (c * LPR + q) * S::CE;
+      if (g.wide_out) {
+        if (has && e0 < N) store_cell<S::CE>(row_out + e0, o);
+      } else {  // (a lane's own cell)
+        store_cell_of<S>(mine, q, c, o);
+      }
+    }
+    if (!g.wide_out) {
       // rows that are not aligned: through shared memory, so that neighbouring
-      // lanes write neighbouring elements (each lane its own cell's, the 33 MB
-      // of 16383 x 250 gradients took 28 us)
-      __syncwarp();
-#pragma unroll
-      for (int c = 0; c < S::C; ++c)
-#pragma unroll
-        for (int h = 0; h < S::CE; h += 4) {
-          const float* v = o + c * S::CE + h;
-          *reinterpret_cast<float4*>(mine + (c * LPR + q) * S::CE + h) = make_float4(v[0], v[1], v[2], v[3]);
-        }
+      // lanes write neighbouring elements
       __syncwarp();
       for (int i = q; i < N; i += LPR) {
-        if (has) row_out[i] = from_f32<Tl>(mine[i]);
-        mine[i] = 0.f;
+        const int at = slot_of<S>(i);
+        if (has) row_out[i] = from_f32<Tl>(mine[at]);
+        mine[at] = 0.f;
       }
       __syncwarp();
     }
     if (g.dgates && g.wide_out) {  // every lane has read its cells
       __syncwarp();
-      if (e >= 0) mine[e] = 0.f;
+      if (e >= 0) mine[slot_of<S>(e)] = 0.f;
       __syncwarp();
     }
   }
