@@ -247,8 +247,10 @@ int launch_clip(const bfmoe_grad* g, int n, float max_norm, float* norm, double*
 // shared by 2 or 4 rows of a warp.  65536 x 256 gradients: 38 us with 32 lanes
 // of 8 logits.
 template <class F>
-cudaError_t with_shape(int N, F&& f) {
+cudaError_t with_shape(int N, bool cells, F&& f) {
   if (N <= 64) return f(RowShape<8, 8>{});
+  if (!cells && N <= 128) return f(RowShape<16, 8>{});
+  if (!cells && N <= 256) return f(RowShape<32, 8>{});
   if (N <= 128) return f(RowShape<8, 16>{});
   if (N <= 256) return f(RowShape<16, 16>{});
   if (N <= 512) return f(RowShape<32, 16>{});
@@ -342,7 +344,7 @@ template <typename Tl>
 cudaError_t launch_balance(const Logits<Tl>& x, int T, int N, int k, bool sigmoid, const int32_t* idx, float* part, double* zpart,
                            int32_t* loads, int* grid, cudaStream_t s) {
   if (N <= 1024)
-    return with_shape(N, [&](auto shape) {
+    return with_shape(N, wide_rows<RowShape<32, 8>>(x.p, x.ld, N), [&](auto shape) {
       using S = decltype(shape);
       if (sigmoid) return launch_balance_rows<S, true>(x, T, N, k, idx, part, zpart, loads, grid, s);
       return launch_balance_rows<S, false>(x, T, N, k, idx, part, zpart, loads, grid, s);
@@ -384,7 +386,7 @@ template <typename Tl>
 cudaError_t launch_route_backward(const Logits<Tl>& x, int T, int N, int k, const RouteCfg& cfg, const RouteGrad& g,
                                   cudaStream_t s) {
   if (N <= 1024)
-    return with_shape(N, [&](auto shape) {
+    return with_shape(N, wide_rows<RowShape<32, 8>>(x.p, x.ld, N), [&](auto shape) {
       using S = decltype(shape);
       const bool sigmoid = cfg.score == BFMOE_SCORE_SIGMOID;
       // losses, and gates that are a softmax of the whole row, reach every logit

@@ -622,7 +622,7 @@ enum { kByLogit = 0, kBySoftmax = 1, kBySigmoid = 2 };
 
 // Blocks of an SM: what the registers of a row leave room for.
 template <class S>
-constexpr int kRouteBlocks = S::V <= 8 ? 4 : 3;
+constexpr int kRouteBlocks = 3;
 
 // Floats of shared memory for the group values of a row: all values in 64 bits
 // where there is room for them.
