@@ -457,23 +457,27 @@ struct RawRow {
     for (int c = 0; c < S::C; ++c)
       load_cell<false>(c, reinterpret_cast<const Tl*>(row) + (c * S::LPR + q) * S::CE, true);
   }
-  // The logits, NaN as -inf; of bfloat16, whose equal values meet as keys, -0
-  // as 0.
+  // The logits; FIX: NaN as -inf.
+  template <bool FIX>
   __device__ __forceinline__ void unpack(bool wide, float (&l)[S::V]) const {
     if constexpr (BF16) {
       if (wide) {
 #pragma unroll
         for (int i = 0; i < S::V / 2; ++i) {
-          l[2 * i] = fmaxf(__uint_as_float(w[i] << 16), -INFINITY) + 0.f;
-          l[2 * i + 1] = fmaxf(__uint_as_float(w[i] & 0xffff0000u), -INFINITY) + 0.f;
+          l[2 * i] = __uint_as_float(w[i] << 16);
+          l[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < S::V; ++i) l[i] = fmaxf(__uint_as_float(w[i] << 16), -INFINITY) + 0.f;
+        for (int i = 0; i < S::V; ++i) l[i] = __uint_as_float(w[i] << 16);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < S::V; ++i) l[i] = fmaxf(__uint_as_float(w[i]), -INFINITY);
+      for (int i = 0; i < S::V; ++i) l[i] = __uint_as_float(w[i]);
+    }
+    if constexpr (FIX) {
+#pragma unroll
+      for (int i = 0; i < S::V; ++i) l[i] = fmaxf(l[i], -INFINITY);
     }
   }
 };
@@ -542,10 +546,11 @@ struct RowFeed {
   // The logits of the warp's rows at t0 (past the end: anything).
   // False after a copy that did not come, which is reported: then nothing of
   // the warp's is on its way any more.
+  template <bool FIX = true>
   __device__ __forceinline__ bool take(const Logits<Tl>& x, int t0, int step, int T, int N, int lane, float (&l)[S::V]) {
     const int q = lane & (S::LPR - 1);
     if constexpr (AHEAD) {
-      raw.unpack(x.wide, l);
+      raw.template unpack<FIX>(x.wide, l);
       if (t0 + step < T) raw.load(x, min(t0 + step + lane / S::LPR, T - 1), N, q);
     } else {
       if (staged) {
@@ -563,7 +568,7 @@ struct RowFeed {
       } else {
         raw.load(x, min(t0 + lane / S::LPR, T - 1), N, q);
       }
-      raw.unpack(x.wide, l);
+      raw.template unpack<FIX>(x.wide, l);
     }
     if (!x.wide) {
       float* cells = reinterpret_cast<float*>(buf) + lane / S::LPR * S::MAXN;
@@ -580,7 +585,7 @@ struct RowFeed {
     if constexpr (!AHEAD) {
       if (here) {
         raw.load_shared(here, lane & (S::LPR - 1));
-        raw.unpack(x.wide, l);
+        raw.template unpack<true>(x.wide, l);
       } else {
         load_cells<S>(reinterpret_cast<const float*>(buf) + lane / S::LPR * S::MAXN, lane & (S::LPR - 1), l);
       }
@@ -611,9 +616,9 @@ __device__ __forceinline__ float row_softmax(const float (&l)[S::V], float m, fl
 
 template <class S>
 __device__ __forceinline__ float row_max(const float (&l)[S::V]) {
-  float h = l[0];
+  float h = -INFINITY;
 #pragma unroll
-  for (int i = 1; i < S::V; ++i) h = fmaxf(h, l[i]);
+  for (int i = 0; i < S::V; ++i) h = fmaxf(h, l[i]);  // drops NaN
   return seg_max<S::LPR>(h);
 }
 // What ranks the experts: the logits, or softmax or sigmoid scores (with a
@@ -698,7 +703,8 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
              full_s + w * 2);
   for (; t < T; t += step) {
     float l[V], c[V];
-    if (!feed.take(x, t, step, T, N, lane, l)) return;
+    // (by logits, NaN stay: they fail every comparison)
+    if (!feed.template take<BY != kByLogit>(x, t, step, T, N, lane, l)) return;
     float m = 0.f, inv_z = 1.f;
     if constexpr (BY == kBySoftmax) {
       m = row_max<S>(l);
@@ -964,9 +970,9 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
       for (int i = 0; i < V; ++i)
         if (!((allowed >> i) & 1u)) c[i] = -INFINITY;
     }
-    float h = c[0];
+    float h = -INFINITY;
 #pragma unroll
-    for (int i = 1; i < V; ++i) h = fmaxf(h, c[i]);
+    for (int i = 0; i < V; ++i) h = fmaxf(h, c[i]);
     // threshold
     const uint32_t first = ordered(h);
     uint32_t key = first, last = 0u;
@@ -999,11 +1005,19 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
     if constexpr (SCORED) {
       if (bias && least < INFINITY) least -= 2.f * value_eps(eps_s, softmax, 1.f, least);
     }
+    // who reaches it: bit V - 1 - i for value i (the sign of the difference to
+    // the next lower number: 0 and -0 are equal, and so is who is it)
     unsigned want = 0u;
+    if (fabsf(least) < INFINITY) {
+      least = from_ordered(ordered(least) - 1u);
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (c[i] >= least) want |= 1u << i;
-    want &= allowed;
+      for (int i = 0; i < V; ++i) want = __funnelshift_l(__float_as_uint(c[i] - least), want, 1);
+      want = ~want;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) want = want << 1 | (least < 0.f || c[i] == least);
+    }
+    want &= __brev(allowed) >> (32 - V);
     // candidates into lanes
     int n = 0;
     for (;;) {
@@ -1011,7 +1025,7 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
       if (!b) break;
       const int at = n + __popc(b & ((1u << lane) - 1u));
       if (want) {
-        const int i = __ffs(want) - 1;
+        const int i = V - __ffs(want);
         if (at < 32) cand[at].e = ((i / CE) * LPR + lane) * CE + i % CE;
         want &= want - 1u;
       }
@@ -1025,7 +1039,12 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
       if (softmax && !cfg.renorm) {
         if constexpr (GROUPED) m = row_max<S>(l);
         else m = from_ordered(__reduce_max_sync(FULL_MASK, first));
-        const float z = row_softmax<S>(l, m, c);
+        float z = row_softmax<S>(l, m, c);
+        if (z != z) {  // NaN among the logits
+#pragma unroll
+          for (int i = 0; i < V; ++i) l[i] = fmaxf(l[i], -INFINITY);
+          z = row_softmax<S>(l, m, c);
+        }
         inv_z = z > 0.f ? rcp_fast(z) : 0.f;
       }
     }

@@ -38,17 +38,33 @@ struct TwoSided {
 // sigmoid(-l) in t; masked logits give 0 and 1.  Where softmax terms x =
 // exp(l - m) are at hand and the largest logit is moderate, sigmoid(l) is
 // x / (x + exp(-m)): no second exponential.
-__device__ __forceinline__ bool moderate(float m) { return !__any_sync(FULL_MASK, !(m >= -10.f && m <= 40.f)); }
+__device__ __forceinline__ bool moderate(float m) { return !__any_sync(FULL_MASK, !(m >= -10.f && m <= 20.f)); }
+// 1 / (x + c) for a row's x in [0, 1] and c in [e^-20, e^10], in r: four
+// reciprocals from one (products of four stay within float32; the special
+// function unit, 16 results a clock and SM, is what bounds the losses).
+template <class S>
+__device__ __forceinline__ void row_reciprocals(const float (&x)[S::V], float c, float (&r)[S::V]) {
+#pragma unroll
+  for (int i = 0; i < S::V; i += 4) {
+    const float a0 = x[i] + c, a1 = x[i + 1] + c, a2 = x[i + 2] + c, a3 = x[i + 3] + c;
+    const float p = a0 * a1, q = a2 * a3, one = rcp_fast(p * q);
+    const float rp = one * q, rq = one * p;
+    r[i] = rp * a1;
+    r[i + 1] = rp * a0;
+    r[i + 2] = rq * a3;
+    r[i + 3] = rq * a2;
+  }
+}
 template <class S>
 __device__ __forceinline__ void row_sigmoid(const float (&l)[S::V], float m, bool has_x, const float (&x)[S::V],
                                             float (&u)[S::V], float (&t)[S::V]) {
   if (has_x && moderate(m)) {
     const float c = exp_fast(-m);
+    row_reciprocals<S>(x, c, t);
 #pragma unroll
     for (int i = 0; i < S::V; ++i) {
-      const float r = rcp_fast(x[i] + c);
-      t[i] = c * r;
-      u[i] = x[i] * r;
+      u[i] = x[i] * t[i];
+      t[i] *= c;
     }
     return;
   }
@@ -106,9 +122,10 @@ __global__ __launch_bounds__(kGradWarps * 32, kBalanceRowBlocks<S>) void balance
     float inv;
     if constexpr (SIGMOID) {
       if (moderate(m)) {
-        const float c = exp_fast(-m);
+        float r[V];
+        row_reciprocals<S>(u, exp_fast(-m), r);
 #pragma unroll
-        for (int i = 0; i < V; ++i) u[i] *= rcp_fast(u[i] + c);
+        for (int i = 0; i < V; ++i) u[i] *= r[i];
       } else {
         float c[V];
         feed.again(x, min(t, T - 1), N, lane, l);
