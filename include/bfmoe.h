@@ -417,7 +417,8 @@ int bfmoe_route(const void* logits, int dtype, int T, long long ld, int n_expert
  *   load      device int32 [N + 1] (written): load_e, then R.  Loads of
  *             several ranks may be added up before bfmoe_route_backward.
  *   ws        as for bfmoe_route
- * Sums are float64 across rows of blocks, in a fixed order.
+ * Sums are float32 over a block's rows and float64 over the blocks, in a fixed
+ * order.
  */
 int bfmoe_balance_loss(const void* logits, int dtype, int T, long long ld, int n_experts, int k, int score,
                        const int32_t* idx, float* loss, int32_t* load, void* ws, size_t ws_bytes,
@@ -426,6 +427,8 @@ int bfmoe_balance_loss(const void* logits, int dtype, int T, long long ld, int n
 /*
  * Gradient of the logits: through the gates of bfmoe_route (the choice is
  * held, as in bfmoe_backward) and through the two losses, in one pass.
+ *   balance_bias  device float [N] or NULL, as for bfmoe_route: an expert that
+ *             it masks has no gate and so no gradient from it
  *   idx       device int32 [T][k]: the routing (may be NULL without dgates)
  *   dgates    device float [T][k]: the gradient of the gates, or NULL
  *   load      device int32 [N + 1] of bfmoe_balance_loss, or NULL (no losses)
@@ -433,14 +436,15 @@ int bfmoe_balance_loss(const void* logits, int dtype, int T, long long ld, int n
  *             with load
  *   dlogits   device [T] rows of N, ld_dlogits apart, dtype of the logits
  *             (written, 0 for masked experts); may be the logits themselves
+ *             (with their row stride), else they do not overlap
  * An index out of range is skipped and recorded as BFMOE_EDEVICE_BOUNDS.
  * What is left of the router's gradient are plain matrix products:
  * dW_g = dlogits^T x, db = column sums, dx += dlogits W_g.
  */
 int bfmoe_route_backward(const void* logits, int dtype, int T, long long ld, int n_experts, int k,
-                         const bfmoe_scoring* scoring, const int32_t* idx, const float* dgates,
-                         const int32_t* load, const float* dloss, void* dlogits, long long ld_dlogits,
-                         bfmoe_stream_t stream);
+                         const bfmoe_scoring* scoring, const float* balance_bias, const int32_t* idx,
+                         const float* dgates, const int32_t* load, const float* dloss, void* dlogits,
+                         long long ld_dlogits, bfmoe_stream_t stream);
 
 /* Scratch bytes of bfmoe_route and bfmoe_balance_loss (0 for invalid sizes). */
 size_t bfmoe_route_workspace_size(int n_experts, int T, int k);

@@ -136,7 +136,8 @@ def balance_loss(logits, idx, score="softmax"):
     return (N * float((f * P / rows).sum()), z / rows), load, rows
 
 
-def route_backward_row(l, idx, score="softmax", renorm=True, scale=1.0, dgates=None, load=None, rows=0, dloss=(0.0, 0.0)):
+def route_backward_row(l, idx, score="softmax", renorm=True, scale=1.0, dgates=None, load=None, rows=0,
+                       dloss=(0.0, 0.0), bias=None):
     """(gradient [N], bound [N]): the gradient of one row, and the sum of the
     magnitudes of the terms it is made of (what rounding errors scale with)."""
     l = np.asarray(l, np.float64)
@@ -148,8 +149,10 @@ def route_backward_row(l, idx, score="softmax", renorm=True, scale=1.0, dgates=N
     s = softmax_row(l) if score == "softmax" else sigmoid_row(l)
     one_minus = 1.0 - s if score == "softmax" else np.where(live, sigmoid_row(-np.where(live, l, 0.0)), 0.0)
     if dgates is not None:
-        dg = np.asarray(dgates, np.float64) * scale
         ok = live[idx]
+        if bias is not None:
+            ok = ok & live_mask(np.asarray(bias, np.float64))[idx]
+        dg = np.where(ok, np.asarray(dgates, np.float64), 0.0) * scale
         if score == "softmax" and not renorm:
             pc = np.where(ok, s[idx], 0.0)
             dot, mag = float((pc * dg).sum()), float(np.abs(pc * dg).sum())

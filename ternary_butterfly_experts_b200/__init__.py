@@ -470,10 +470,13 @@ def bfmoe_route_workspace_size(n_experts: int, T: int, k: int) -> int:
     return int(capi.lib().bfmoe_route_workspace_size(n_experts, T, k))
 
 
-def _route_ws(ws, N, T, k, dev):
-    if ws is None:
-        n = bfmoe_route_workspace_size(N, T, k)
-        return _torch().empty(max(n, 256), dtype=_torch().uint8, device=dev)
+def _scratch(n, dev, stream):
+    """A workspace of one call.  It is freed when the call returns: a stream
+    other than the current one is told that it still uses it."""
+    torch = _torch()
+    ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    if stream is not None:
+        ws.record_stream(stream)
     return ws
 
 
@@ -493,7 +496,7 @@ def bfmoe_router_logits(x, w_gate, bias=None, logits=None, ws=None, stream=None)
     _need_shape(logits, "logits", torch.float32, T, N)
     s = _here(stream, "x", x, "w_gate", w_gate, "bias", bias, "logits", logits, "ws", ws)
     if ws is None:
-        ws = workspace(d, N, T, 1, code, x.device)
+        ws = _scratch(bfmoe_workspace_size(d, N, T, 1, code), x.device, stream)
     capi.check(capi.lib().bfmoe_router_logits(_ptr(x), code, T, d, _ptr(w_gate), _ptr(bias), N, _ptr(logits),
                                               _ptr(ws), ws.numel(), s))
     return logits
@@ -524,7 +527,7 @@ def bfmoe_route(logits, k: int, scoring: Scoring, balance_bias=None, ws=None, ou
         s = _here(stream, "logits", logits, "balance_bias", balance_bias, "idx", idx, "gates", gates,
                   "counts", counts, "offsets", offsets, "rows", rows, "ws", ws)
     if counts is not None and ws is None:
-        ws = _route_ws(ws, N, T, k, logits.device)
+        ws = _scratch(bfmoe_route_workspace_size(N, T, k), logits.device, stream)
     capi.check(capi.lib().bfmoe_route(
         logits.data_ptr(), code, T, ld, N, k, scoring.ref, _ptr(balance_bias), _ptr(idx), _ptr(gates),
         _ptr(counts), _ptr(offsets), _ptr(rows), _ptr(ws), ws.nbytes if ws is not None else 0, s))
@@ -550,17 +553,18 @@ def bfmoe_balance_loss(logits, idx, score: str = "softmax", ws=None, out=None, s
     _need_shape(load, "load", torch.int32, N + 1)
     s = _here(stream, "logits", logits, "idx", idx, "loss", loss, "load", load, "ws", ws)
     if ws is None:
-        ws = _route_ws(ws, N, T, k, logits.device)
+        ws = _scratch(bfmoe_route_workspace_size(N, T, k), logits.device, stream)
     capi.check(capi.lib().bfmoe_balance_loss(logits.data_ptr(), code, T, ld, N, k, Scoring.SCORES[score], _ptr(idx),
                                              loss.data_ptr(), load.data_ptr(), ws.data_ptr(), ws.nbytes, s))
     return out
 
 
 def bfmoe_route_backward(logits, idx, scoring: Scoring, dgates=None, load=None, dloss=None, dlogits=None,
-                         stream=None):
+                         balance_bias=None, stream=None):
     """Gradient of the logits [T][N] (their dtype) from ``dgates`` [T,k], the
     gradient of bfmoe_route's gates, and from ``dloss`` [2], that of
-    bfmoe_balance_loss's losses, with its ``load``."""
+    bfmoe_balance_loss's losses, with its ``load``.  ``balance_bias`` is needed
+    where it masks experts (-inf)."""
     torch = _torch()
     code, T, N, ld = _logits(logits)
     if idx.dim() != 2:
@@ -570,15 +574,17 @@ def bfmoe_route_backward(logits, idx, scoring: Scoring, dgates=None, load=None, 
     _need_shape(dgates, "dgates", torch.float32, T, k)
     _need_shape(load, "load", torch.int32, N + 1)
     _need_shape(dloss, "dloss", torch.float32, 2)
+    _need_shape(balance_bias, "balance_bias", torch.float32, N)
     if dlogits is None:
         dlogits, ldd = logits.new_empty((T, N)), N
     else:
         if dlogits.dtype is not logits.dtype or dlogits.shape != logits.shape:
             raise ValueError("dlogits must match logits in shape and dtype")
         ldd = _logits(dlogits, "dlogits")[3]
-    s = _here(stream, "logits", logits, "idx", idx, "dgates", dgates, "load", load, "dloss", dloss, "dlogits", dlogits)
+    s = _here(stream, "logits", logits, "idx", idx, "dgates", dgates, "load", load, "dloss", dloss, "dlogits", dlogits,
+              "balance_bias", balance_bias)
     capi.check(capi.lib().bfmoe_route_backward(
-        logits.data_ptr(), code, T, ld, N, k, scoring.ref, _ptr(idx), _ptr(dgates), _ptr(load), _ptr(dloss),
+        logits.data_ptr(), code, T, ld, N, k, scoring.ref, _ptr(balance_bias), _ptr(idx), _ptr(dgates), _ptr(load), _ptr(dloss),
         dlogits.data_ptr(), ldd, s))
     return dlogits
 
@@ -604,7 +610,7 @@ def bfmoe_expert_backward(layer: "Layer", x, k: int, routing, gy, ws=None, strea
     s = _here(stream, "x", x, "gy", gy, "idx", idx, "gates", gates, "offsets", offsets, "rows", rows,
               "theta", layer.theta, "ws", ws)
     if ws is None:
-        ws = torch.empty(max(bfmoe_backward_workspace_size(d, N, T, k), 256), dtype=torch.uint8, device=x.device)
+        ws = _scratch(bfmoe_backward_workspace_size(d, N, T, k), x.device, stream)
     f = dict(dtype=torch.float32, device=x.device)
     out = {"dx": torch.empty((T, d), **f), "dtheta": torch.empty_like(layer.theta),
            "dphi": torch.empty_like(layer.phi), "dw_base": torch.empty((d, d), **f),
@@ -669,7 +675,11 @@ class GradList:
 def _grad_call(grads, norm, stream):
     """(GradList, norm, stream handle) of a call on the current device."""
     torch = _torch()
-    g = grads if isinstance(grads, GradList) else GradList(grads)
+    g = grads
+    if not isinstance(g, GradList):
+        g = GradList(grads)
+        if stream is not None:  # the list's workspace goes when the call returns
+            g.ws.record_stream(stream)
     if norm is None:
         norm = g.ws.new_empty(1, dtype=torch.float32)
     else:

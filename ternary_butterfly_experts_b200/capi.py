@@ -89,7 +89,7 @@ SIGNATURES = {
     "bfmoe_router_logits": (_I, [_P, _I, _I, _I, _P, _P, _I, _P, _P, _SZ, _P]),
     "bfmoe_route": (_I, [_P, _I, _I, _LL, _I, _I, _SCORING, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "bfmoe_balance_loss": (_I, [_P, _I, _I, _LL, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
-    "bfmoe_route_backward": (_I, [_P, _I, _I, _LL, _I, _I, _SCORING, _P, _P, _P, _P, _P, _LL, _P]),
+    "bfmoe_route_backward": (_I, [_P, _I, _I, _LL, _I, _I, _SCORING, _P, _P, _P, _P, _P, _P, _LL, _P]),
     "bfmoe_route_workspace_size": (_SZ, [_I, _I, _I]),
     "bfmoe_expert_backward": (_I, [ctypes.POINTER(BfmoeLayer), _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                    _P, _P, _SZ, _P]),

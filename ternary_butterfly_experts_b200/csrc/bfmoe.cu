@@ -1545,6 +1545,7 @@ int bfmoe_check_device_error(bfmoe_stream_t stream) {
     // the other translation unit's kernels record in its own word
     if ((e = take_route_error(&code, &info)) != cudaSuccess) return cuda_fail(e, "read error word");
     if (code == 0) return ok();
+    if (code == BFMOE_EDEVICE_TIMEOUT) return fail(BFMOE_EDEVICE_TIMEOUT, "device wait timed out (site 0x%x)", info);
     return fail(static_cast<int>(code), "device check failed (code %u, at %u)", code, info);
   }
   const unsigned zero = 0;

@@ -65,6 +65,24 @@ __device__ __forceinline__ int grad_of_chunk(const G& g, int c) {
   return lo;
 }
 
+// Bytes at the end of the list that the norm leaves in L2 for the scaling, which
+// begins there: what lies before is loaded to be replaced first.  (189 MB of
+// bfloat16: 95.7 us without it, 92.5 with 48 MB, 90.5 with 80, 91.3 with 108.)
+constexpr long long kGradKept = 80LL << 20;
+
+__device__ __forceinline__ uint64_t evict_first_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void bulk_load_hint(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
 // A chunk of a tensor: `vecs` 16-byte vectors from element `at` on are in
 // shared memory; `head` elements before `at` and `tail` behind them are not.
 struct GradChunk {
@@ -78,10 +96,11 @@ struct GradChunk {
 // Chunks first, first + step, ... (count of them) through the ring.  The
 // consumer threads call ready() once, while the first copies are on their way;
 // where it says so use(chunk, vectors) for every chunk, else the copies stop
-// there.  Every wait is bounded; after one that ran out all return, the
+// there.  Chunks before `kept` are the first that L2 replaces.  Every wait is
+// bounded; after one that ran out all return, the
 // producer after its own copies.
 template <class G, class R, class F>
-__device__ __forceinline__ void grad_stream(const G& g, int first, int step, int count, R&& ready, F&& use) {
+__device__ __forceinline__ void grad_stream(const G& g, int first, int step, int count, int kept, R&& ready, F&& use) {
   extern __shared__ __align__(128) uint8_t grad_ring[];
   __shared__ uint64_t full[kGradStages], empty[kGradStages], go;
   __shared__ GradChunk meta[kGradStages];
@@ -108,6 +127,7 @@ __device__ __forceinline__ void grad_stream(const G& g, int first, int step, int
     if (threadIdx.x == kGradConsumers) {
       int q = 0;
       bool done = false;
+      const uint64_t policy = evict_first_policy();
       // the tensor at hand: its list entry is read once
       int c0 = 0, c1 = 0, sh = 0, head = 0;
       long long len = 0;
@@ -142,9 +162,12 @@ __device__ __forceinline__ void grad_stream(const G& g, int first, int step, int
         }
         meta[s] = m;
         mbar_expect_tx(full + s, m.vecs * 16);
-        if (m.vecs > 0)
-          bulk_load(grad_ring + s * kGradChunkBytes, static_cast<const uint8_t*>(m.src) + (m.at << sh), m.vecs * 16,
-                    full + s);
+        if (m.vecs > 0) {
+          void* to = grad_ring + s * kGradChunkBytes;
+          const void* from = static_cast<const uint8_t*>(m.src) + (m.at << sh);
+          if (c < kept) bulk_load_hint(to, from, m.vecs * 16, full + s, policy);
+          else bulk_load(to, from, m.vecs * 16, full + s);
+        }
       }
       // the copies in flight where nobody takes them any more
       if (q <= stages && !done) done = mbar_wait(&go, 0, 0x2204u) ? !going : true;
@@ -235,7 +258,8 @@ __global__ __launch_bounds__(kGradThreads, kGradBlocks) void grad_norm_kernel(co
   uint32_t top = 0;
   const int chunks = g.first[g.n];
   const int mine = (chunks - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
-  grad_stream(g, blockIdx.x, gridDim.x, mine, [] { return true; }, [&](const GradChunk& m, const uint4* v) {
+  const int kept = chunks - static_cast<int>(kGradKept / kGradChunkBytes);
+  grad_stream(g, blockIdx.x, gridDim.x, mine, kept, [] { return true; }, [&](const GradChunk& m, const uint4* v) {
     const bool bf16 = m.src_bf16;
     if (bf16) {
 #pragma unroll 4
@@ -340,7 +364,7 @@ __global__ __launch_bounds__(kGradThreads, kGradBlocks) void grad_scale_kernel(c
   pdl_trigger();
   GradFactor f{};
   const int last = g.first[g.n] - 1 - static_cast<int>(blockIdx.x);
-  grad_stream(g, last, -static_cast<int>(gridDim.x), last / static_cast<int>(gridDim.x) + 1,
+  grad_stream(g, last, -static_cast<int>(gridDim.x), last / static_cast<int>(gridDim.x) + 1, 0x7fffffff,
               [&] {
                 pdl_wait();
                 const double v = grad_total(part, parts);

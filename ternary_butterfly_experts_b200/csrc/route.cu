@@ -63,7 +63,8 @@ int check_routing_sizes(const char* what, int N, long long T, int k, long long l
   if (N < 1 || N > BFMOE_MAX_EXPERTS) return fail(BFMOE_EINVAL, "%s: n_experts=%d must be in [1, %d]", what, N, BFMOE_MAX_EXPERTS);
   if (k < 1 || k > BFMOE_MAX_K || k > N) return fail(BFMOE_EINVAL, "%s: k=%d must be in [1, min(%d, N=%d)]", what, k, BFMOE_MAX_K, N);
   if (T < 0) return fail(BFMOE_EINVAL, "%s: T=%lld must be >= 0", what, T);
-  if (T * k > 0x7fffffffLL) return fail(BFMOE_EUNSUPPORTED, "%s: T*k=%lld exceeds int32 row ids", what, T * k);
+  // (row ids, and the strides of grids over the rows, are int32)
+  if (T * k > 0x7ff00000LL) return fail(BFMOE_EUNSUPPORTED, "%s: T*k=%lld exceeds int32 row ids", what, T * k);
   if (ld < N) return fail(BFMOE_EINVAL, "%s: row stride %lld is less than n_experts=%d", what, ld, N);
   if (dtype != BFMOE_F32 && dtype != BFMOE_BF16) return fail(BFMOE_EINVAL, "%s: dtype=%d is not BFMOE_F32 or BFMOE_BF16", what, dtype);
   return BFMOE_OK;
@@ -490,8 +491,9 @@ int bfmoe_balance_loss(const void* logits, int dtype, int T, long long ld, int n
 }
 
 int bfmoe_route_backward(const void* logits, int dtype, int T, long long ld, int n_experts, int k,
-                         const bfmoe_scoring* scoring, const int32_t* idx, const float* dgates, const int32_t* load,
-                         const float* dloss, void* dlogits, long long ld_dlogits, bfmoe_stream_t stream) {
+                         const bfmoe_scoring* scoring, const float* balance_bias, const int32_t* idx,
+                         const float* dgates, const int32_t* load, const float* dloss, void* dlogits,
+                         long long ld_dlogits, bfmoe_stream_t stream) {
   const int N = n_experts;
   int rc = check_routing_sizes("route_backward", N, T, k, ld, dtype);
   if (rc || (rc = check_scoring("route_backward", scoring, N, k))) return rc;
@@ -505,7 +507,7 @@ int bfmoe_route_backward(const void* logits, int dtype, int T, long long ld, int
   if (logits == dlogits && ld != ld_dlogits) return fail(BFMOE_EINVAL, "route_backward: in place with another row stride");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const RouteCfg cfg = cfg_of(scoring);
-  const RouteGrad g{idx, dgates, load, dloss, dlogits, ld_dlogits, 0};
+  const RouteGrad g{idx, balance_bias, dgates, load, dloss, dlogits, ld_dlogits, 0};
   const cudaError_t e =
       dtype == BFMOE_BF16
           ? launch_route_backward(Logits<__nv_bfloat16>{static_cast<const __nv_bfloat16*>(logits), ld, 0}, T, N, k, cfg, g, s)

@@ -379,6 +379,7 @@ __device__ __forceinline__ void store_cell(__nv_bfloat16* p, const float* v) {
 
 struct RouteGrad {
   const int32_t* idx;
+  const float* bias;     // balance bias, or NULL: only where it masks
   const float* dgates;   // or NULL
   const int32_t* load;   // or NULL
   const float* dloss;
@@ -466,7 +467,6 @@ __global__ __launch_bounds__(kGradWarps * 32, ROW ? kGradRowBlocks<S> : 4) void 
     ask_logit(next, t0 + step + lane / LPR);
     ask(after, t0 + 2 * step + lane / LPR);
     int e = now.e;
-    const float dg = now.dg * cfg.scale;
     // the chosen
     float le = -INFINITY;
     bool live = false;
@@ -479,8 +479,9 @@ __global__ __launch_bounds__(kGradWarps * 32, ROW ? kGradRowBlocks<S> : 4) void 
         if constexpr (ROW) le = feed.at(x, t, e);
         else le = now.l;
       }
-      live = e >= 0 && !masked_logit(le);
+      live = e >= 0 && !masked_logit(le) && !(g.bias && masked_logit(g.bias[e]));
     }
+    const float dg = live ? now.dg * cfg.scale : 0.f;
     float m = 0.f, inv = 0.f, pa = 0.f, lse = 0.f;
     if constexpr (ROW) {
       m = row_max<S>(l);
@@ -617,7 +618,8 @@ __global__ __launch_bounds__(kGradWarps * 32) void route_backward_long_kernel(co
           dg = g.dgates[static_cast<long long>(t) * k + lane] * cfg.scale;
         }
       }
-      const bool live = e >= 0 && !masked_logit(l);
+      const bool live = e >= 0 && !masked_logit(l) && !(g.bias && masked_logit(g.bias[e]));
+      if (!live) dg = 0.f;
       if (dense) {
         d = live ? unit_softmax(l, r.m) * inv_z * dg : 0.f;
         dot = warp_sum(d);

@@ -349,6 +349,52 @@ def test_backward_masked_rows(N):
                 check_backward(t, l, 3, score, renorm, 1.5, aux=False)
 
 
+@pytest.mark.parametrize("N", [12, 250, 1024, 1300])
+def test_backward_of_masked_choices(N):
+    """Chosen experts that a logit or the bias masks have no gate: no gradient from it, whatever theirs is
+    (NaN included), and none of the others' gradient passes through them."""
+    T, k = 9, 4
+    t, _ = make_logits(T, N, "f32", N + 3)
+    t[:, : N - 3] = float("-inf")           # three experts are left, one of them masked by the bias
+    l = t.double().numpy()
+    bias = np.zeros(N, np.float32)
+    bias[N - 2] = -np.inf
+    db = torch.from_numpy(bias).cuda()
+    for score in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            sc = scoring(score, renorm=renorm)
+            idx, gates = B().bfmoe_route(t.cuda(), k, sc, balance_bias=db, buckets=False)[:2]
+            ref, g = S.route(l, k, bias=bias, score=score, renorm=renorm)
+            assert np.array_equal(idx.cpu().numpy(), ref)
+            off = (torch.from_numpy(g) == 0).cuda()
+            assert int(off.sum()) == 2 * T
+            dg = torch.randn(T, k, device="cuda")
+            dg[off] = float("nan")
+            got = B().bfmoe_route_backward(t.cuda(), idx, sc, dgates=dg, balance_bias=db).double().cpu().numpy()
+            want, bound = S.route_backward(l, ref, dgates=dg.cpu().numpy(), score=score, renorm=renorm, bias=bias)
+            assert np.isfinite(got).all()
+            assert (np.abs(got - want) <= half_steps(l) * bound + TINY).all()
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, each with its workspace, and calls on a stream that is not current,
+    whose workspace the binding makes."""
+    T, N, k = 4000, 256, 8
+    sc = scoring("sigmoid", groups=8, top_groups=4, group_score="top2")
+    xs = [make_logits(T, N, "f32", s)[0].cuda() for s in (1, 2)]
+    want = [B().bfmoe_route(x, k, sc) for x in xs]
+    losses = [B().bfmoe_balance_loss(x, w[0], "sigmoid") for x, w in zip(xs, want)]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [B().bfmoe_route(x, k, sc, stream=s) for x, s in zip(xs, streams)]
+        more = [B().bfmoe_balance_loss(x, g[0], "sigmoid", stream=s) for x, g, s in zip(xs, got, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got + more, want + losses):
+            for p, q in zip(a, b):
+                assert torch.equal(p, q)
+
+
 def test_backward_repeated_and_foreign_indices():
     """The same expert twice adds up; an index out of range is reported and skipped."""
     t, l = make_logits(9, 40, "f32", 3)

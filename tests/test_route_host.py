@@ -38,6 +38,7 @@ def test_route_refuses(L):
         assert route(L, **kw) == EINVAL, kw
     assert L.bfmoe_route(64, F32, 4, 8, 8, 2, None, None, 64, 64, 64, 64, 64, 256, 1 << 30, None) == EINVAL
     assert route(L, T=1 << 30, k=8) == EUNS
+    assert route(L, T=0x7ff00001, k=1) == EUNS
     for ws in ((None, 0), (256, 16), (264, 1 << 30)):
         assert route(L, ws=ws) == EWS
     # no tokens and no buckets: nothing to do
@@ -64,8 +65,8 @@ def test_route_backward_refuses(L):
     n0 = L.bfmoe_launch_count()
 
     def f(logits=64, dtype=F32, T=4, ld=8, N=8, k=2, s=None, idx=64, dg=64, load=64, dloss=64, out=64, ldd=8):
-        return L.bfmoe_route_backward(logits, dtype, T, ld, N, k, s if s is not None else sc(), idx, dg, load, dloss,
-                                      out, ldd, None)
+        return L.bfmoe_route_backward(logits, dtype, T, ld, N, k, s if s is not None else sc(), None, idx, dg, load,
+                                      dloss, out, ldd, None)
 
     for kw in (dict(ldd=7), dict(load=None), dict(dloss=None), dict(logits=None), dict(out=None), dict(idx=None),
                dict(out=66), dict(ld=10, ldd=8), dict(s=sc(score=9)), dict(k=0), dict(dtype=4)):
