@@ -650,8 +650,8 @@ struct Candidate {
 // each other by value and index.  (Picking the largest k + 1 times instead,
 // with every value made into a sortable key, took 820 instructions a row of
 // 1024 experts for k = 4; this takes half.)
-// A row with more than 32 candidates (many equal values) is left to
-// route_row_64.
+// Rows with more than 32 candidates (many equal values) are left for the end,
+// to route_row_64.
 //
 // Scores are float32 and rank two values rightly only where they are further
 // apart than their errors.  The threshold is lowered by both, and where two
@@ -660,7 +660,7 @@ struct Candidate {
 template <class S, typename Tl, int BY, bool GROUPED>
 __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_kernel(
     const Logits<Tl> x, int T, int N, int k, const RouteCfg cfg, const float* __restrict__ bias, int lsh,
-    int32_t* __restrict__ idx, float* __restrict__ gates) {
+    int32_t* idx, float* __restrict__ gates) {
   constexpr int LPR = 32, V = S::V, CE = S::CE, C = S::C;
   static_assert(S::LPR == 32);
   constexpr bool SCORED = BY != kByLogit;
@@ -701,6 +701,7 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
              reinterpret_cast<uint8_t*>(route_smem + (SCORED ? S::MAXN : 0) + (GROUPED ? kRouteWarps * kGroupSpace<S> : 0)) +
                  w * RowFeed<S, Tl>::bytes(x.wide),
              full_s + w * 2);
+  bool left = false;
   for (; t < T; t += step) {
     float l[V], c[V];
     // (by logits, NaN stay: they fail every comparison)
@@ -1103,16 +1104,22 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
         gates[static_cast<long long>(t) * k + rank] = u * cfg.scale;
       }
     } else {
-      int e2;
-      float g2;
-      __syncwarp();
-      route_row_64(x, t, N, k, cfg, bias, reinterpret_cast<int*>(cand), lane, e2, g2);
-      if (lane < k) {
-        idx[static_cast<long long>(t) * k + lane] = e2;
-        gates[static_cast<long long>(t) * k + lane] = g2;
-      }
+      if (lane == 0) idx[static_cast<long long>(t) * k] = -1;
+      left = true;
     }
     __syncwarp();  // the candidates and group values are read before the next row's are written
+  }
+  if (!left) return;
+  // the rows left over (marked by the warp itself above)
+  for (t = blockIdx.x * kRouteWarps + w; t < T; t += step) {
+    if (__shfl_sync(FULL_MASK, lane == 0 ? idx[static_cast<long long>(t) * k] : 0, 0) >= 0) continue;
+    int e;
+    float g;
+    route_row_64(x, t, N, k, cfg, bias, reinterpret_cast<int*>(cand), lane, e, g);
+    if (lane < k) {
+      idx[static_cast<long long>(t) * k + lane] = e;
+      gates[static_cast<long long>(t) * k + lane] = g;
+    }
   }
 }
 
