@@ -871,7 +871,12 @@ cudaError_t build_buckets(const int32_t* idx, long long R, int k, int N, bool ha
     e = launch("bucket_count", s, [&] { bucket_count_kernel<<<nchunks, chunk, N * 4, s>>>(idx, R, N, cc); });
     if (e != cudaSuccess) return e;
   }
-  e = launch("bucket_scan", s, [&] { pdl_launch(bucket_scan_kernel, (N + 31) / 32, 1024, 0, s, cc, nchunks, N, totals); });
+  e = launch("bucket_scan", s, [&] {
+    if (nchunks >= 256)
+      pdl_launch(bucket_scan_few_kernel, (N + kScanFewExperts - 1) / kScanFewExperts, 1024, 0, s, cc, nchunks, N, totals);
+    else
+      pdl_launch(bucket_scan_kernel, (N + 31) / 32, 1024, 0, s, cc, nchunks, N, totals);
+  });
   if (e != cudaSuccess) return e;
   const size_t scatter_smem = ((N + 1) * 4 + 15) / 16 * 16 + static_cast<size_t>(N) * 36 + 4;
   return launch("bucket_scatter", s, [&] {

@@ -37,6 +37,43 @@ __global__ __launch_bounds__(1024) void bucket_count_kernel(const int32_t* __res
   for (int e = threadIdx.x; e < N; e += blockDim.x) dst[e] = cnt[e];
 }
 
+// bucket_scan_kernel with 8 experts a block by 128 chunk slices, for 256 chunks
+// and more: four times the blocks (1024 chunks of 1024 experts: 7.9 us instead
+// of 13.4; 128 chunks of 256 experts: 5.5 either way).
+constexpr int kScanFewExperts = 8;
+__global__ __launch_bounds__(1024) void bucket_scan_few_kernel(int32_t* __restrict__ chunk_counts, int nchunks, int N,
+                                                               int32_t* __restrict__ totals) {
+  constexpr int X = kScanFewExperts;
+  __shared__ int part[32][X];  // rows of each expert in the slices of each warp
+  pdl_wait();
+  pdl_trigger();
+  const int tx = threadIdx.x % X, ty = threadIdx.x / X, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int e = blockIdx.x * X + tx;
+  const int per = (nchunks + 1024 / X - 1) / (1024 / X);
+  const int c0 = min(ty * per, nchunks), c1 = min(c0 + per, nchunks);
+  int s = 0;
+  if (e < N)
+    for (int c = c0; c < c1; ++c) s += chunk_counts[static_cast<size_t>(c) * N + e];
+  int incl = s;
+#pragma unroll
+  for (int o = X; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(FULL_MASK, incl, o);
+    if (lane >= o) incl += t;
+  }
+  if (lane >= 32 - X) part[w][tx] = incl;
+  __syncthreads();
+  int run = incl - s;
+  for (int q = 0; q < w; ++q) run += part[q][tx];
+  if (e < N && threadIdx.x >= 1024 - X) totals[e] = run + s;
+  if (e < N)
+    for (int c = c0; c < c1; ++c) {
+      const size_t a = static_cast<size_t>(c) * N + e;
+      const int tmp = chunk_counts[a];
+      chunk_counts[a] = run;
+      run += tmp;
+    }
+}
+
 // Block of 32 experts (x) by 32 chunk slices (y).  Rewrites chunk_counts
 // into exclusive prefixes over chunks; totals[e] = rows of expert e.
 __global__ __launch_bounds__(1024) void bucket_scan_kernel(int32_t* __restrict__ chunk_counts, int nchunks, int N,
