@@ -48,13 +48,14 @@ RoutePlan make_route_plan(int N, long long T, int k) {
   };
   const long long nchunks = std::max(1LL, (T + 127) / 128);
   (void)k;
+  const size_t blocks = static_cast<size_t>(std::max(1LL, std::min<long long>(T, kBalanceBlocks)));
   p.chunk_counts = take(static_cast<size_t>(nchunks) * N * 4);
   p.totals = take(static_cast<size_t>(N) * 4);
   const size_t buckets_end = off;
   off = 0;
-  p.part = take(static_cast<size_t>(kBalanceBlocks) * N * 4);
-  p.zpart = take(static_cast<size_t>(kBalanceBlocks) * 8);
-  p.loads = take(static_cast<size_t>(kBalanceBlocks) * (N + 1) * 4);
+  p.part = take(blocks * N * 4);
+  p.zpart = take(blocks * 8);
+  p.loads = take(blocks * (N + 1) * 4);
   p.total = std::max(buckets_end, off);
   return p;
 }

@@ -100,11 +100,13 @@ __device__ __noinline__ double score_64(float l, float M, double Z, bool softmax
   return softmax ? x / Z : 1.0 / (1.0 + x);
 }
 
-// Float32 scores are off by less than this times their size (softmax: the sum
-// collects half a step a term at worst, and an exponent x of exp carries |x|
-// half steps, |x| p <= 0.37) ...
+// Float32 scores are off by less than this times their size: softmax, in half
+// steps, 2.5 for each unit of the exponent (|x| p <= 0.37, and 17 on average
+// over the sum: |x| <= ln N), 7 of the functions and products, one for each
+// addition of the sum at worst, 16 for the rounding of m log2 e where |m| < 16 is
+// folded into the exponents (row_softmax) ...
 __device__ __forceinline__ float score_eps(bool softmax, int terms) {
-  return 0x1p-23f * (softmax ? 24.f + 0.5f * static_cast<float>(terms) : 4.f);
+  return 0x1p-23f * (softmax ? 32.f + 0.5f * static_cast<float>(terms) : 4.f);
 }
 // ... and a value by its score's error and its own rounding.
 __device__ __forceinline__ float value_eps(float eps_s, bool softmax, float score, float value) {
@@ -611,7 +613,7 @@ __device__ __forceinline__ float lane_sum(const float (&v)[V]) {
 // exp(l - m) of a row and its sum over the row; masked logits give 0.
 template <class S>
 __device__ __forceinline__ float row_softmax(const float (&l)[S::V], float m, float (&u)[S::V]) {
-  if (fabsf(m) < 0x1p120f) {
+  if (fabsf(m) < 16.f) {
     const float2 by = make_float2(1.4426950408889634f, 1.4426950408889634f);
     const float2 ml = make_float2(-m * by.x, -m * by.x);
 #pragma unroll
@@ -620,6 +622,9 @@ __device__ __forceinline__ float row_softmax(const float (&l)[S::V], float m, fl
       u[i] = exp2_fast(x.x);
       u[i + 1] = exp2_fast(x.y);
     }
+  } else if (fabsf(m) < 0x1p120f) {
+#pragma unroll
+    for (int i = 0; i < S::V; ++i) u[i] = exp_fast(l[i] - m);
   } else {  // +-inf, or masks of the type's lowest value alone
 #pragma unroll
     for (int i = 0; i < S::V; ++i) u[i] = masked_logit(l[i]) ? 0.f : unit_softmax(l[i], m);
@@ -639,8 +644,7 @@ __device__ __forceinline__ float row_max(const float (&l)[S::V]) {
 enum { kByLogit = 0, kBySoftmax = 1, kBySigmoid = 2 };
 
 // Blocks of an SM.  (16384 x 256 in groups, with buckets: 30.4 us with 3 blocks
-// of 80 registers a thread, 33.0 with 4 of 64; 131072 x 1024: the routing alone
-// 121 us with 3, 182 with 2 of 128 in an earlier form.)
+// of 80 registers a thread, 33.0 with 4 of 64.)
 template <class S>
 constexpr int kRouteBlocks = 3;
 
@@ -664,7 +668,7 @@ struct Candidate {
 // 256 or 1024 for k = 8): those are the candidates, one a lane, ranked among
 // each other by value and index.  (Picking the largest k + 1 times instead,
 // with every value made into a sortable key, took 174 us for 131072 rows of
-// 1024 experts, k = 4; this takes 105: 5.1 TB/s, bound by the instructions
+// 1024 experts, k = 4; this takes 107: 5.1 TB/s, bound by the instructions
 // issued, about 500 a row.)
 // Rows with more than 32 candidates (many equal values) are left for the end,
 // to route_row_64.

@@ -192,6 +192,22 @@ def test_route_near_ties(N):
         check_route(torch.from_numpy(up), up.astype(np.float64), 8, **kw)
 
 
+@pytest.mark.parametrize("shift", [-300.0, 25.0, 400.0, 5000.0])
+def test_route_shifted_logits(shift):
+    """A shift of every logit changes no softmax; near values are ranked as in 64 bits all the same."""
+    for N in (64, 256, 1024):
+        rng = np.random.default_rng(N)
+        l = (rng.normal(size=(60, N)) + shift).astype(np.float32)
+        p = np.exp(l[0].astype(np.float64) - l[0].max())
+        bias = (0.3 - p / p.sum()).astype(np.float32)   # row 0: every value next to 0.3
+        l[1:] = l[0]
+        l[np.arange(1, 60), rng.integers(0, N, 59)] += np.float32(1e-3)
+        check_route(torch.from_numpy(l), l.astype(np.float64), 6, bias=bias, renorm=False)
+        check_route(torch.from_numpy(l), l.astype(np.float64), 6, score="sigmoid", bias=bias)
+        check_backward(torch.from_numpy(l[:9]), l[:9].astype(np.float64), 3, "softmax", False, 1.0)
+        check_backward(torch.from_numpy(l[:9]), l[:9].astype(np.float64), 3, "sigmoid", True, 1.0)
+
+
 def test_route_strided_and_unaligned_rows():
     for dtype in (torch.float32, torch.bfloat16):
         for N, ld, off in ((256, 300, 1), (64, 67, 3), (250, 256, 2), (1024, 1029, 5), (1500, 1501, 1)):
