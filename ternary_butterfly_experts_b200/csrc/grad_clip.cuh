@@ -15,8 +15,9 @@ namespace bfmoe {
 // Streaming: a producer warp walks the list in chunks and copies each into a
 // ring in shared memory (bulk copies), 16 consumer warps take them from there,
 // so that loads are in flight while the list is searched and squares are
-// summed.  189 MB of bfloat16: norm 39 us (4.8 TB/s; bound by the instructions
-// of the float64 squares), scaling 51 us (7.4 TB/s, part of it from L2).  (With
+// summed.  One tensor: norm at 5.7 TB/s for 189 MB, 6.8 for 1.5 GB of float32
+// (6.2 of bfloat16), bound by memory.  189 MB of bfloat16 in 144 tensors: norm
+// 39 us, scaling 51 us (7.4 TB/s, part of it from L2).  (With
 // loads into registers, 4 blocks of 512 threads an SM and four 16-byte loads a
 // thread, the norm took 47 us: between a block's chunks nothing was in flight.)
 constexpr int kGradsPerLaunch = 512;
@@ -97,8 +98,7 @@ struct GradChunk {
 // consumer threads call ready() once, while the first copies are on their way;
 // where it says so use(chunk, vectors) for every chunk, else the copies stop
 // there.  Chunks before `kept` are the first that L2 replaces.  Every wait is
-// bounded; after one that ran out all return, the
-// producer after its own copies.
+// bounded; after one that ran out all return, the producer after its own copies.
 template <class G, class R, class F>
 __device__ __forceinline__ void grad_stream(const G& g, int first, int step, int count, int kept, R&& ready, F&& use) {
   extern __shared__ __align__(128) uint8_t grad_ring[];
@@ -222,30 +222,15 @@ __device__ __forceinline__ void add_square(double& s, float x) {
   s = fma(v, v, s);
 }
 
-// The squares of a vector.  bfloat16 becomes float64 without the conversion
-// unit (16 a clock and SM, half of what memory delivers): |x|'s bits moved to a
-// float64's are x 2^-896, zero and subnormal numbers included, and one product
-// with 2^896 makes them x.  Infinities and NaN come out finite: top, the
-// largest |x| of the two halves as integers, tells of them.
+// The squares of a vector.  (Making the float64 of a bfloat16 from its bits, to
+// spare the conversion unit, which takes 16 a clock and SM: 34.8 us instead of
+// 33.1 for one tensor of 189 MB, 242 instead of 245 for 1.5 GB.)
 template <typename T>
-__device__ __forceinline__ void square_vector(double (&s)[4], uint32_t& top, const uint4& u) {
-  if constexpr (sizeof(T) == 4) {
-    float f[4];
-    grad_unpack<T>(u, f);
+__device__ __forceinline__ void square_vector(double (&s)[4], const uint4& u) {
+  float f[kGradVec<T>];
+  grad_unpack<T>(u, f);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) add_square(s[q], f[q]);
-  } else {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const double a = __hiloint2double(static_cast<int>((w[q] << 13) & 0x0fffe000u), 0) * 0x1p896;
-      const double b = __hiloint2double(static_cast<int>((w[q] >> 3) & 0x0fffe000u), 0) * 0x1p896;
-      s[q] = fma(a, a, s[q]);
-      s[q ^ 1] = fma(b, b, s[q ^ 1]);
-    }
-    top = __vimax3_u16x2(top, w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu);
-    top = __vimax3_u16x2(top, w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu);
-  }
+  for (int q = 0; q < kGradVec<T>; ++q) add_square(s[q & 3], f[q]);
 }
 
 template <int MAX>
@@ -255,7 +240,6 @@ __global__ __launch_bounds__(kGradThreads, kGradBlocks) void grad_norm_kernel(co
   pdl_wait();
   pdl_trigger();
   double s[4] = {0.0, 0.0, 0.0, 0.0};
-  uint32_t top = 0;
   const int chunks = g.first[g.n];
   const int mine = (chunks - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
   const int kept = chunks - static_cast<int>(kGradKept / kGradChunkBytes);
@@ -263,10 +247,10 @@ __global__ __launch_bounds__(kGradThreads, kGradBlocks) void grad_norm_kernel(co
     const bool bf16 = m.src_bf16;
     if (bf16) {
 #pragma unroll 4
-      for (int i = threadIdx.x; i < m.vecs; i += kGradConsumers) square_vector<__nv_bfloat16>(s, top, v[i]);
+      for (int i = threadIdx.x; i < m.vecs; i += kGradConsumers) square_vector<__nv_bfloat16>(s, v[i]);
     } else {
 #pragma unroll 4
-      for (int i = threadIdx.x; i < m.vecs; i += kGradConsumers) square_vector<float>(s, top, v[i]);
+      for (int i = threadIdx.x; i < m.vecs; i += kGradConsumers) square_vector<float>(s, v[i]);
     }
     if (static_cast<int>(threadIdx.x) < m.head + m.tail) {
       const int r = threadIdx.x;
@@ -276,8 +260,6 @@ __global__ __launch_bounds__(kGradThreads, kGradBlocks) void grad_norm_kernel(co
     }
   });
   if (threadIdx.x >= kGradConsumers) return;
-  const uint32_t t = max(top & 0xffffu, top >> 16);
-  if (t >= 0x7f80u) s[0] += static_cast<double>(__uint_as_float(t << 16));  // infinity or NaN
   const double sum = consumer_sum((s[0] + s[1]) + (s[2] + s[3]), red);
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
