@@ -391,6 +391,8 @@ typedef struct {
  *     bits from the given logits and bias.
  *   - gates: the scores of the chosen (no bias; 0 for a masked expert), over
  *     their sum when renormalize (all 0 where nothing is left), times scale.
+ *     A score below the smallest normal float32 may come out as 0, here and in
+ *     the losses and gradients below.
  *   logits    device [T] rows of N, ld elements apart (ld >= N), dtype
  *   balance_bias  device float [N] or NULL
  *   idx, gates, counts, offsets, rows: as bfmoe_router_topk writes them; the
