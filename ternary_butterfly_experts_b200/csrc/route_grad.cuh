@@ -299,6 +299,8 @@ __global__ __cluster_dims__(kFinishBlocks, 1, 1) __launch_bounds__(kFinishThread
   while (width < per) width <<= 1;
   const int slices = kFinishThreads / width, e = rank * per + (tid & (width - 1)), slice = tid / width;
   const bool real = (tid & (width - 1)) < per && e < N;
+  // (waited for before the store into block 0's memory: block 0 runs by then)
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   pdl_wait();
   pdl_trigger();
   double p = 0.0;
@@ -330,6 +332,7 @@ __global__ __cluster_dims__(kFinishBlocks, 1, 1) __launch_bounds__(kFinishThread
     if (tid < s) ps[tid] += ps[tid + s];
     __syncthreads();
   }
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (tid == 0) {
     uint32_t there;
     asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(there) : "r"(smem_u32(share + rank)));
