@@ -12,6 +12,7 @@ applies B(theta)^T, the ternary product and B(phi) without forming W_i
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import struct
@@ -53,6 +54,26 @@ def _stream(stream=None):
     if raw is not None:
         return raw(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
+
+
+_CURRENT = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Where a call makes its outputs and scratch: in the memory pool of the
+    stream that it runs on.  A block of another stream's pool may still be in
+    use there, by work that this call is not ordered behind."""
+    return _CURRENT if stream is None else _torch().cuda.stream(stream)
+
+
+def _returned(stream, *tensors):
+    """Outputs made for a call on ``stream``: the caller, on the current
+    stream, uses them too, so they are not reused before that stream is done."""
+    if stream is not None:
+        here = _torch().cuda.current_stream()
+        for t in tensors:
+            if t is not None:
+                t.record_stream(here)
 
 
 def _ptr(t):
@@ -471,13 +492,10 @@ def bfmoe_route_workspace_size(n_experts: int, T: int, k: int) -> int:
 
 
 def _scratch(n, dev, stream):
-    """A workspace of one call.  It is freed when the call returns: a stream
-    other than the current one is told that it still uses it."""
+    """A workspace of one call, freed when the call returns."""
     torch = _torch()
-    ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws
+    with _on(stream):
+        return torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
 
 
 def bfmoe_router_logits(x, w_gate, bias=None, logits=None, ws=None, stream=None):
@@ -492,7 +510,9 @@ def bfmoe_router_logits(x, w_gate, bias=None, logits=None, ws=None, stream=None)
     _need_shape(bias, "bias", torch.float32, N)
     code = _dtype_code(x)
     if logits is None:
-        logits = torch.empty((T, N), dtype=torch.float32, device=x.device)
+        with _on(stream):
+            logits = torch.empty((T, N), dtype=torch.float32, device=x.device)
+        _returned(stream, logits)
     _need_shape(logits, "logits", torch.float32, T, N)
     s = _here(stream, "x", x, "w_gate", w_gate, "bias", bias, "logits", logits, "ws", ws)
     if ws is None:
@@ -513,8 +533,10 @@ def bfmoe_route(logits, k: int, scoring: Scoring, balance_bias=None, ws=None, ou
     _need_shape(balance_bias, "balance_bias", torch.float32, N)
     if out is None:
         new, i32 = logits.new_empty, torch.int32
-        out = (new((T, k), dtype=i32), new((T, k), dtype=torch.float32))
-        out += (new(N, dtype=i32), new(N + 1, dtype=i32), new(T * k, dtype=i32)) if buckets else (None, None, None)
+        with _on(stream):
+            out = (new((T, k), dtype=i32), new((T, k), dtype=torch.float32))
+            out += (new(N, dtype=i32), new(N + 1, dtype=i32), new(T * k, dtype=i32)) if buckets else (None, None, None)
+        _returned(stream, *out)
         idx, gates, counts, offsets, rows = out
         s = _here(stream, "logits", logits, "balance_bias", balance_bias, "ws", ws)
     else:
@@ -547,7 +569,9 @@ def bfmoe_balance_loss(logits, idx, score: str = "softmax", ws=None, out=None, s
     k = idx.shape[1]
     _need_shape(idx, "idx", torch.int32, T, k)
     if out is None:
-        out = (logits.new_empty(2, dtype=torch.float32), logits.new_empty(N + 1, dtype=torch.int32))
+        with _on(stream):
+            out = (logits.new_empty(2, dtype=torch.float32), logits.new_empty(N + 1, dtype=torch.int32))
+        _returned(stream, *out)
     loss, load = out
     _need_shape(loss, "loss", torch.float32, 2)
     _need_shape(load, "load", torch.int32, N + 1)
@@ -576,7 +600,9 @@ def bfmoe_route_backward(logits, idx, scoring: Scoring, dgates=None, load=None, 
     _need_shape(dloss, "dloss", torch.float32, 2)
     _need_shape(balance_bias, "balance_bias", torch.float32, N)
     if dlogits is None:
-        dlogits, ldd = logits.new_empty((T, N)), N
+        with _on(stream):
+            dlogits, ldd = logits.new_empty((T, N)), N
+        _returned(stream, dlogits)
     else:
         if dlogits.dtype is not logits.dtype or dlogits.shape != logits.shape:
             raise ValueError("dlogits must match logits in shape and dtype")
@@ -612,9 +638,11 @@ def bfmoe_expert_backward(layer: "Layer", x, k: int, routing, gy, ws=None, strea
     if ws is None:
         ws = _scratch(bfmoe_backward_workspace_size(d, N, T, k), x.device, stream)
     f = dict(dtype=torch.float32, device=x.device)
-    out = {"dx": torch.empty((T, d), **f), "dtheta": torch.empty_like(layer.theta),
-           "dphi": torch.empty_like(layer.phi), "dw_base": torch.empty((d, d), **f),
-           "dalpha": torch.empty((1,), **f), "dgates": torch.empty((T, k), **f)}
+    with _on(stream):
+        out = {"dx": torch.empty((T, d), **f), "dtheta": torch.empty_like(layer.theta),
+               "dphi": torch.empty_like(layer.phi), "dw_base": torch.empty((d, d), **f),
+               "dalpha": torch.empty((1,), **f), "dgates": torch.empty((T, k), **f)}
+    _returned(stream, *out.values())
     capi.check(capi.lib().bfmoe_expert_backward(
         ctypes.byref(layer.c), _ptr(x), _dtype_code(x), T, k, _ptr(idx), _ptr(gates), _ptr(offsets), _ptr(rows),
         _ptr(gy), _ptr(out["dx"]), _ptr(out["dtheta"]), _ptr(out["dphi"]), _ptr(out["dw_base"]), _ptr(out["dalpha"]),
@@ -631,7 +659,8 @@ class GradList:
     and bfmoe_grad_clip, with its workspace: made once, used every step while
     the tensors stay where they are.  ``out``: tensors of the same shapes that
     bfmoe_grad_clip writes instead of scaling in place (None entries: in place).
-    Calls that overlap on the GPU need a list each (they share its workspace)."""
+    Calls that overlap on the GPU need a list each (they share its workspace,
+    which is made on the stream that is current here)."""
 
     def __init__(self, grads, out=None):
         torch = _torch()
@@ -677,11 +706,14 @@ def _grad_call(grads, norm, stream):
     torch = _torch()
     g = grads
     if not isinstance(g, GradList):
-        g = GradList(grads)
-        if stream is not None:  # the list's workspace goes when the call returns
-            g.ws.record_stream(stream)
+        with _on(stream):  # the list's workspace goes when the call returns
+            g = GradList(grads)
+    elif stream is not None:
+        g.ws.record_stream(stream)
     if norm is None:
-        norm = g.ws.new_empty(1, dtype=torch.float32)
+        with _on(stream):
+            norm = g.ws.new_empty(1, dtype=torch.float32)
+        _returned(stream, norm)
     else:
         _need_shape(norm, "norm", torch.float32, 1)
     return g, norm, _here(stream, "the gradients", g.ws, "norm", norm)
