@@ -138,7 +138,9 @@ def bfmoe_pack_base(w, out=None, stream=None):
     if w.dim() != 2 or w.shape[0] != d:
         raise ValueError("w must be [d][d]")
     if out is None:
-        out = torch.empty((d, words_per_row(d)), dtype=torch.int32, device=w.device)
+        with _on(stream):
+            out = torch.empty((d, words_per_row(d)), dtype=torch.int32, device=w.device)
+        _returned(stream, out)
     capi.check(capi.lib().bfmoe_pack_base(_ptr(w), d, _ptr(out), _stream(stream)))
     return out
 
@@ -148,9 +150,32 @@ def bfmoe_unpack_base(w_packed, d: int, out=None, stream=None):
     torch = _torch()
     _need(w_packed, "w_packed")
     if out is None:
-        out = torch.empty((d, d), dtype=torch.bfloat16, device=w_packed.device)
+        with _on(stream):
+            out = torch.empty((d, d), dtype=torch.bfloat16, device=w_packed.device)
+        _returned(stream, out)
     capi.check(capi.lib().bfmoe_unpack_base(_ptr(w_packed), d, _ptr(out), _stream(stream)))
     return out
+
+
+def _routing_buffers(T, N, k, dev, stream, buckets=True):
+    """(idx, gates, counts, offsets, rows) for a call on ``stream``."""
+    torch = _torch()
+    with _on(stream):
+        out = (torch.empty((T, k), dtype=torch.int32, device=dev),
+               torch.empty((T, k), dtype=torch.float32, device=dev))
+        out += (torch.empty((N,), dtype=torch.int32, device=dev),
+                torch.empty((N + 1,), dtype=torch.int32, device=dev),
+                torch.empty((T * k,), dtype=torch.int32, device=dev)) if buckets else (None, None, None)
+    _returned(stream, *out)
+    return out
+
+
+def _like(x, stream):
+    """An output of x's shape and type for a call on ``stream``."""
+    with _on(stream):
+        y = _torch().empty_like(x)
+    _returned(stream, y)
+    return y
 
 
 def bfmoe_router_topk(x, w_gate, bias, k: int, ws, out=None, stream=None, buckets: bool = True):
@@ -165,11 +190,7 @@ def bfmoe_router_topk(x, w_gate, bias, k: int, ws, out=None, stream=None, bucket
     N = w_gate.shape[0]
     dev = x.device
     if out is None:
-        out = (torch.empty((T, k), dtype=torch.int32, device=dev),
-               torch.empty((T, k), dtype=torch.float32, device=dev))
-        out += (torch.empty((N,), dtype=torch.int32, device=dev),
-                torch.empty((N + 1,), dtype=torch.int32, device=dev),
-                torch.empty((T * k,), dtype=torch.int32, device=dev)) if buckets else (None, None, None)
+        out = _routing_buffers(T, N, k, dev, stream, buckets)
     idx, gates, counts, offsets, rows = out
     capi.check(capi.lib().bfmoe_router_topk(
         _ptr(x), _dtype_code(x), T, d, _ptr(w_gate), _ptr(bias), N, k, _ptr(idx), _ptr(gates),
@@ -193,11 +214,7 @@ def bfmoe_router_topk_noalloc(x, w_gate, bias, k: int, out=None, stream=None):
     N = w_gate.shape[0]
     dev = x.device
     if out is None:
-        out = (torch.empty((T, k), dtype=torch.int32, device=dev),
-               torch.empty((T, k), dtype=torch.float32, device=dev),
-               torch.empty((N,), dtype=torch.int32, device=dev),
-               torch.empty((N + 1,), dtype=torch.int32, device=dev),
-               torch.empty((T * k,), dtype=torch.int32, device=dev))
+        out = _routing_buffers(T, N, k, dev, stream)
     idx, gates, counts, offsets, rows = out
     capi.check(capi.lib().bfmoe_router_topk_noalloc(
         _ptr(x), _dtype_code(x), T, d, _ptr(w_gate), _ptr(bias), N, k, _ptr(idx), _ptr(gates),
@@ -229,7 +246,9 @@ class Layer:
         this layer read them instead of rebuilding them per call."""
         torch = _torch()
         n = bfmoe_layer_tables_size(self.d, self.n_experts)
-        self.tables = torch.empty(max(n, 256), dtype=torch.uint8, device=self.theta.device)
+        with _on(stream):
+            self.tables = torch.empty(max(n, 256), dtype=torch.uint8, device=self.theta.device)
+        _returned(stream, self.tables)
         self.c.tables = None
         bfmoe_prepare_layer(self, self.tables, stream=stream)
         self.c.tables = self.tables.data_ptr()
@@ -248,7 +267,9 @@ class Layer:
         _need(w_gate, "w_gate", torch.float32)
         N, d = w_gate.shape
         n = int(capi.lib().bfmoe_gate_parts_size(N, d))
-        self.gate_parts = torch.empty(max(n, 256), dtype=torch.uint8, device=w_gate.device)
+        with _on(stream):
+            self.gate_parts = torch.empty(max(n, 256), dtype=torch.uint8, device=w_gate.device)
+        _returned(stream, self.gate_parts)
         capi.check(capi.lib().bfmoe_prepare_gate(_ptr(w_gate), N, d, _ptr(self.gate_parts), self.gate_parts.numel(),
                                                 _stream(stream)))
         self.c.gate_parts = self.gate_parts.data_ptr()
@@ -296,13 +317,12 @@ def bfmoe_prepare_layer(layer: "Layer", tables, stream=None):
 
 def bfmoe_forward(layer: Layer, x, k: int, idx, gates, offsets, rows, ws, y=None, stream=None):
     """y [T][d] (dtype of x) = sum_j g_j B(phi) (alpha W_base (B(theta)^T x))."""
-    torch = _torch()
     _need(x, "x")
     T, d = x.shape
     if d != layer.d:
         raise ValueError(f"x has width {d}, layer has d={layer.d}")
     if y is None:
-        y = torch.empty_like(x)
+        y = _like(x, stream)
     capi.check(capi.lib().bfmoe_forward(
         ctypes.byref(layer.c), _ptr(x), _dtype_code(x), T, k, _ptr(idx), _ptr(gates), _ptr(offsets),
         _ptr(rows), _ptr(y), _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)))
@@ -320,7 +340,7 @@ def bfmoe_decode_forward(layer: Layer, x, k: int, idx, gates, y=None, stream=Non
     _need(idx, "idx", torch.int32)
     _need(gates, "gates", torch.float32)
     if y is None:
-        y = torch.empty_like(x)
+        y = _like(x, stream)
     capi.check(capi.lib().bfmoe_decode_forward(
         ctypes.byref(layer.c), _ptr(x), _dtype_code(x), T, k, _ptr(idx), _ptr(gates), _ptr(y), _stream(stream)))
     return y
@@ -346,13 +366,14 @@ def bfmoe_backward(layer: Layer, x, k: int, w_gate, routing, gy, bias_grad: bool
     idx, gates, _counts, offsets, rows = routing
     dev = x.device
     if ws is None:
-        n = bfmoe_backward_workspace_size(d, N, T, k)
-        ws = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+        ws = _scratch(bfmoe_backward_workspace_size(d, N, T, k), dev, stream)
     f = dict(dtype=torch.float32, device=dev)
-    out = {"dx": torch.empty((T, d), **f), "dtheta": torch.empty_like(layer.theta),
-           "dphi": torch.empty_like(layer.phi), "dw_base": torch.empty((d, d), **f),
-           "dalpha": torch.empty((1,), **f), "dw_gate": torch.empty((N, d), **f),
-           "dbias": torch.empty((N,), **f) if bias_grad else None}
+    with _on(stream):
+        out = {"dx": torch.empty((T, d), **f), "dtheta": torch.empty_like(layer.theta),
+               "dphi": torch.empty_like(layer.phi), "dw_base": torch.empty((d, d), **f),
+               "dalpha": torch.empty((1,), **f), "dw_gate": torch.empty((N, d), **f),
+               "dbias": torch.empty((N,), **f) if bias_grad else None}
+    _returned(stream, *out.values())
     capi.check(capi.lib().bfmoe_backward(
         ctypes.byref(layer.c), _ptr(x), _dtype_code(x), T, k, _ptr(w_gate), _ptr(idx), _ptr(gates), _ptr(offsets),
         _ptr(rows), _ptr(gy), _ptr(out["dx"]), _ptr(out["dtheta"]), _ptr(out["dphi"]), _ptr(out["dw_base"]),
@@ -378,13 +399,9 @@ def bfmoe_moe_forward(layer: Layer, x, w_gate, bias, k: int, ws, routing=None, y
     N = layer.n_experts
     dev = x.device
     if routing is None:
-        routing = (torch.empty((T, k), dtype=torch.int32, device=dev),
-                   torch.empty((T, k), dtype=torch.float32, device=dev),
-                   torch.empty((N,), dtype=torch.int32, device=dev),
-                   torch.empty((N + 1,), dtype=torch.int32, device=dev),
-                   torch.empty((T * k,), dtype=torch.int32, device=dev))
+        routing = _routing_buffers(T, N, k, dev, stream)
     if y is None:
-        y = torch.empty_like(x)
+        y = _like(x, stream)
     idx, gates, counts, offsets, rows = routing
     capi.check(capi.lib().bfmoe_moe_forward(
         ctypes.byref(layer.c), _ptr(x), _dtype_code(x), T, _ptr(w_gate), _ptr(bias), k, _ptr(idx), _ptr(gates),
@@ -739,7 +756,9 @@ def bfmoe_materialize_expert(layer: Layer, e: int, out=None, stream=None):
     """alpha * B(phi_e) . W_base . B(theta_e)^T as float32 [d][d] (checking aid)."""
     torch = _torch()
     if out is None:
-        out = torch.empty((layer.d, layer.d), dtype=torch.float32, device=layer.theta.device)
+        with _on(stream):
+            out = torch.empty((layer.d, layer.d), dtype=torch.float32, device=layer.theta.device)
+        _returned(stream, out)
     capi.check(capi.lib().bfmoe_materialize_expert(ctypes.byref(layer.c), e, _ptr(out), _stream(stream)))
     return out
 
@@ -859,7 +878,10 @@ class ButterflyMoE:
         if getattr(self, "_host_key", None) != key:
             code = BFMOE_BF16 if self.dtype == torch.bfloat16 else BFMOE_F32
             n = bfmoe_moe_host_workspace_size(self.layer.d, self.layer.n_experts, T, self.k, code, chunk)
-            self.ws_host = torch.empty(max(n, 256), dtype=torch.uint8, device=self.layer.theta.device)
+            self.ws_host = _scratch(n, self.layer.theta.device, stream)
+            _returned(stream, self.ws_host)
             self._host_key = key
+        elif stream is not None:
+            self.ws_host.record_stream(stream)
         return bfmoe_moe_forward_host(self.layer, x_host, self.w_gate, self.bias, self.k, y_host, self.ws_host,
                                       chunk=chunk, stream=stream)

@@ -79,6 +79,7 @@ def watch(monkeypatch):
     monkeypatch.setattr(B, "_stream", lambda s=None: 0 if s is None else s.cuda_stream)
     monkeypatch.setattr(B.capi, "lib", lambda: lib)
     w.lib = lib
+    MODE[:] = [w]
     return w
 
 
@@ -113,6 +114,43 @@ NEW = {
 }
 
 
+def prepared(**kw):
+    a = layer().prepare(**kw)
+    return a.tables
+
+
+def gate_prepared(**kw):
+    a = layer().prepare_gate(dev(N, D), **kw)
+    return a.gate_parts
+
+
+def host_scratch(**kw):
+    moe = B.ButterflyMoE(layer(), dev(N, D), None, K, T, torch.float32)
+    Dev.kept.clear()
+    MODE[0].made.clear()
+    moe.forward_host(torch.ones(T, D), torch.ones(T, D), **kw)
+    return moe.ws_host
+
+
+OLD = {
+    "pack_base": lambda **kw: B.bfmoe_pack_base(dev(D, D, dtype=torch.int8), **kw),
+    "unpack_base": lambda **kw: B.bfmoe_unpack_base(i32(D, 1), D, **kw),
+    "router_topk": lambda **kw: B.bfmoe_router_topk(dev(T, D), dev(N, D), None, K, i32(64), **kw),
+    "router_topk_no_buckets": lambda **kw: B.bfmoe_router_topk(dev(T, D), dev(N, D), None, K, i32(64), buckets=False, **kw),
+    "router_topk_noalloc": lambda **kw: B.bfmoe_router_topk_noalloc(dev(T, D), dev(N, D), None, K, **kw),
+    "forward": lambda **kw: B.bfmoe_forward(layer(), dev(T, D), K, *[routing()[i] for i in (0, 1, 3, 4)], i32(64), **kw),
+    "decode_forward": lambda **kw: B.bfmoe_decode_forward(layer(), dev(T, D), K, *routing()[:2], **kw),
+    "moe_forward": lambda **kw: [t for o in B.bfmoe_moe_forward(layer(), dev(T, D), dev(N, D), None, K, i32(64), **kw)
+                                 for t in ([o] if isinstance(o, torch.Tensor) else o)],
+    "backward": lambda **kw: B.bfmoe_backward(layer(), dev(T, D), K, dev(N, D), routing(), dev(T, D), **kw),
+    "materialize_expert": lambda **kw: B.bfmoe_materialize_expert(layer(), 0, **kw),
+    "prepare": prepared,
+    "prepare_gate": gate_prepared,
+    "forward_host": host_scratch,
+}
+MODE = []
+
+
 def tensors(out):
     if isinstance(out, dict):
         out = out.values()
@@ -142,6 +180,11 @@ def check(watch, call):
 @pytest.mark.parametrize("name", sorted(NEW))
 def test_outputs_and_scratch_belong_to_the_stream_of_the_call(watch, name):
     check(watch, NEW[name])
+
+
+@pytest.mark.parametrize("name", sorted(OLD))
+def test_so_do_those_of_the_layer_calls(watch, name):
+    check(watch, OLD[name])
 
 
 def test_a_kept_list_is_used_on_the_stream_of_the_call(watch):
