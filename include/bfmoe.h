@@ -439,6 +439,8 @@ int bfmoe_balance_loss(const void* logits, int dtype, int T, long long ld, int n
  *   dlogits   device [T] rows of N, ld_dlogits apart, dtype of the logits
  *             (written, 0 for masked experts); may be the logits themselves
  *             (with their row stride), else they do not overlap
+ * Logits of +inf share their row's mass here too: the z loss of such a row is
+ * infinite, its gradient infinite for them and 0 for the others.
  * An index out of range is skipped and recorded as BFMOE_EDEVICE_BOUNDS.
  * What is left of the router's gradient are plain matrix products:
  * dW_g = dlogits^T x, db = column sums, dx += dlogits W_g.

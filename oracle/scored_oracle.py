@@ -187,8 +187,11 @@ def route_backward_row(l, idx, score="softmax", renorm=True, scale=1.0, dgates=N
         b += abs(c) * p * (f + fp) * w
         if dloss[1]:
             top = l[live].max()
-            lse = top + math.log(np.exp(l[live] - top).sum())
-            q = softmax_row(l) * lse * 2 * dloss[1] / rows
+            p = softmax_row(l)
+            if top == np.inf:  # inf for the experts that share the mass, 0 for the others
+                q = np.where(p > 0, np.copysign(np.inf, dloss[1]), 0.0)
+            else:
+                q = p * (top + math.log(np.exp(l[live] - top).sum())) * 2 * dloss[1] / rows
             g += q
             b += np.abs(q)
     return g, b

@@ -508,7 +508,8 @@ __global__ __launch_bounds__(kGradWarps * 32, ROW ? kGradRowBlocks<S> : 4) void 
         s = seg_sum<LPR>(lane_sum(u));
       } else {
         s = row_softmax<S>(l, m, u);
-        lse = m > -INFINITY ? row_lse(m, s) * f.cz : 0.f;
+        // (without a z loss not even of a row with +inf logits: inf times 0)
+        lse = f.cz != 0.f && m > -INFINITY ? row_lse(m, s) * f.cz : 0.f;
       }
       inv = s > 0.f ? rcp_fast(s) : 0.f;
       if (f.cb != 0.f) {
@@ -551,6 +552,9 @@ __global__ __launch_bounds__(kGradWarps * 32, ROW ? kGradRowBlocks<S> : 4) void 
     }
     Tl* row_out = static_cast<Tl*>(g.out) + static_cast<long long>(t) * g.ld_out;
     const float K = lse - pa - dot;  // (softmax)
+    // Sums that are not finite (+inf logits under a z loss, such gradients from
+    // the caller) reach the experts that have a score, not 0 times them the rest.
+    const bool finite = fabsf(SIGMOID ? pa : K) < INFINITY;
 #pragma unroll
     for (int c = 0; c < S::C; ++c) {
       float o[S::CE];
@@ -566,15 +570,15 @@ __global__ __launch_bounds__(kGradWarps * 32, ROW ? kGradRowBlocks<S> : 4) void 
 #pragma unroll
         for (int i = 0; i < S::CE; ++i) {
           const int v = c * S::CE + i;
-          if constexpr (SIGMOID) o[i] = fmaf(u[v] * inv * tt[v], a[i] - pa, o[i]);
-          else o[i] = fmaf(u[v] * inv, a[i] + K, o[i]);
+          const float p = SIGMOID ? u[v] * inv * tt[v] : u[v] * inv;
+          if (finite || p != 0.f) o[i] = fmaf(p, SIGMOID ? a[i] - pa : a[i] + K, o[i]);
         }
         if constexpr (SIGMOID) {
           if (f.cz != 0.f) {
 #pragma unroll
             for (int i = 0; i < S::CE; ++i) {
-              const float v = l[c * S::CE + i];
-              if (!masked_logit(v)) o[i] = fmaf(unit_softmax(v, m), lse, o[i]);
+              const float v = unit_softmax(l[c * S::CE + i], m);
+              if (v > 0.f) o[i] = fmaf(v, lse, o[i]);
             }
           }
         }
@@ -668,14 +672,14 @@ __global__ __launch_bounds__(kGradWarps * 32) void route_backward_long_kernel(co
         const float l = x.at(t, q);
         if (!masked_logit(l)) {
           const float p = dense || f.cb != 0.f || f.cz != 0.f ? unit_softmax(l, r.m) * inv_z : 0.f;
-          if (dense) o -= p * dot;
+          // (where p is 0 the row's sums take no part, finite or not)
+          if (dense && p != 0.f) o -= p * dot;
           if (f.cb != 0.f) {
-            const float ps = sig ? unit_sigmoid(l, low) * inv_s : p;
-            float b = ps * (f.cb * static_cast<float>(g.load[q]) - pa);
-            if (sig) b *= sigmoid_fast(-l);
-            o += b;
+            float ps = sig ? unit_sigmoid(l, low) * inv_s : p;
+            if (sig) ps *= sigmoid_fast(-l);
+            if (ps != 0.f) o += ps * (f.cb * static_cast<float>(g.load[q]) - pa);
           }
-          o += lse * p;
+          if (p != 0.f) o += lse * p;
         }
       }
       for (int j = 0; j < k; ++j) {

@@ -365,6 +365,66 @@ def test_backward_masked_rows(N):
                 check_backward(t, l, 3, score, renorm, 1.5, aux=False)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [6, 64, 250, 256, 1024, 1100])
+def test_backward_of_infinite_logits(N, dtype):
+    """Logits of +inf share the mass: the others' gradient through the row's sums is 0, masked ones have none at all,
+    and only a z loss has an infinite gradient, that of the +inf logits alone."""
+    k = 3
+    t, _ = make_logits(6, N, dtype, N + 2)
+    t[1, N - 1] = float("inf")
+    t[2, [0, N // 2, N - 2]] = float("inf")
+    t[3, 1::2] = float("-inf")
+    t[3, 2] = float("inf")
+    t[4] = float("inf")
+    t[5, : N - 1] = float("nan")
+    t[5, N - 1] = float("inf")
+    l = t.double().numpy()
+    for score in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            check_backward(t, l, k, score, renorm, 1.5, aux=False)
+            check_backward(t, l, k, score, renorm, 1.5, z=0.0)
+            # with a z loss: infinities where the oracle has them, of its sign, the rest as ever
+            idx, _ = S.route(l, k, score=score)
+            _, load, rows = S.balance_loss(l, idx, score)
+            dg = np.random.default_rng(N).normal(size=(6, k)).astype(np.float32)
+            for z in (0.7, -0.7):
+                dl = np.array([0.3, z], np.float32)
+                got = B().bfmoe_route_backward(
+                    t.cuda(), torch.from_numpy(idx.astype(np.int32)).cuda(), scoring(score, renorm=renorm, scale=1.5),
+                    dgates=torch.from_numpy(dg).cuda(), dloss=torch.from_numpy(dl).cuda(),
+                    load=torch.from_numpy(np.append(load, rows).astype(np.int32)).cuda()).double().cpu().numpy()
+                want, bound = S.route_backward(l, idx, score=score, renorm=renorm, scale=1.5, dgates=dg, load=load,
+                                               rows=rows, dloss=tuple(float(v) for v in dl))
+                inf = np.isinf(want)
+                assert (inf == ((l == np.inf) & (np.arange(6) > 0)[:, None])).all()
+                assert np.array_equal(got[inf], want[inf])
+                lim = half_steps(l) * bound[~inf] + TINY
+                if dtype == "bf16":
+                    lim = lim + 2.0 ** -8 * (np.abs(want[~inf]) + lim)
+                assert (np.abs(got[~inf] - want[~inf]) <= lim).all()
+
+
+@pytest.mark.parametrize("N", [12, 250, 1024, 1300])
+def test_backward_of_gate_gradients_that_are_not_finite(N):
+    """A NaN among the gradients of the gates reaches the experts of its row that have a gate; masked experts keep 0,
+    chosen ones among them, and so do the other rows."""
+    T, k = 5, 4
+    t, _ = make_logits(T, N, "f32", N + 4)
+    t[:, : N - 3] = float("-inf")
+    for score in ("softmax", "sigmoid"):
+        for renorm in (False,):
+            sc = scoring(score, renorm=renorm)
+            idx, gates = B().bfmoe_route(t.cuda(), k, sc, buckets=False)[:2]
+            for bad in (float("nan"), float("inf")):
+                dg = torch.randn(T, k, device="cuda")
+                dg[2, 0] = bad
+                got = B().bfmoe_route_backward(t.cuda(), idx, sc, dgates=dg).cpu()
+                assert (got[:, : N - 3] == 0).all(), (score, renorm, bad)
+                assert torch.isfinite(got[[0, 1, 3, 4]]).all()
+                assert not torch.isfinite(got[2]).all()
+
+
 @pytest.mark.parametrize("N", [12, 250, 1024, 1300])
 def test_backward_of_masked_choices(N):
     """Chosen experts that a logit or the bias masks have no gate: no gradient from it, whatever theirs is
