@@ -582,6 +582,13 @@ struct RowFeed {
     }
     return true;
   }
+  // After the rows at t0 were taken, for a warp that takes no more: the copy on
+  // its way is waited for.
+  __device__ __forceinline__ void drain(int t0, int step, int T) {
+    if constexpr (!AHEAD) {
+      if (staged && t0 + step < T) mbar_wait(full + (turn & 1), (turn >> 1) & 1, 0x2102u);
+    }
+  }
   // The row taken last once more (rows of registers are there still).
   __device__ __forceinline__ void again(const Logits<Tl>& x, int t, int N, int lane, float (&l)[S::V]) {
     if constexpr (!AHEAD) {

@@ -408,10 +408,97 @@ struct LossFactors {
       if (R > 0.f) {
         cb = g.dloss[0] * static_cast<float>(N) / R / (static_cast<float>(k) * R);
         cz = 2.f * g.dloss[1] / R;
+        if (!(fabsf(cb) < INFINITY)) {
+          // NaN for every expert that has a score: it comes through the z loss's
+          // factor, which masked experts do not meet
+          cz = cb - cb;
+          cb = 0.f;
+        }
       }
     }
   }
 };
+
+// The gradient of row t by one warp, in several passes over the row.
+template <typename Tl>
+__device__ __noinline__ void route_backward_row(const Logits<Tl>& x, int t, int N, int k, const RouteCfg& cfg,
+                                                const RouteGrad& g, const LossFactors& f, int lane) {
+  const bool sig = cfg.score == BFMOE_SCORE_SIGMOID;
+  const bool dense = g.dgates && !sig && !cfg.renorm;
+  RowSums r{-INFINITY, 0.f, 0.f};
+  if (g.load || dense) r = row_sums(x, t, N, lane, sig);
+  const float low = fminf(r.m, 0.f);
+  const float inv_z = r.z > 0.f ? 1.f / r.z : 0.f, inv_s = r.s > 0.f ? 1.f / r.s : 0.f;
+  int e = -1;
+  float d = 0.f, dot = 0.f;
+  if (g.dgates) {
+    float l = -INFINITY, dg = 0.f;
+    if (lane < k) {
+      e = g.idx[static_cast<long long>(t) * k + lane];
+      if (e < 0 || e >= N) {
+        report_error(BFMOE_EDEVICE_BOUNDS, static_cast<unsigned>(t));
+        e = -1;
+      } else {
+        l = x.at(t, e);
+        dg = g.dgates[static_cast<long long>(t) * k + lane] * cfg.scale;
+      }
+    }
+    const bool live = e >= 0 && !masked_logit(l) && !(g.bias && masked_logit(g.bias[e]));
+    if (!live) dg = 0.f;
+    if (dense) {
+      d = live ? unit_softmax(l, r.m) * inv_z * dg : 0.f;
+      dot = warp_sum(d);
+    } else if (cfg.renorm) {
+      const float m = warp_max(live ? l : -INFINITY);
+      const float u = !live ? 0.f : (sig ? unit_sigmoid(l, fminf(m, 0.f)) : unit_softmax(l, m));
+      const float s = warp_sum(u);
+      const float q = s > 0.f ? u / s : 0.f;
+      d = q * (dg - warp_sum(q * dg));
+    } else {
+      d = live ? dg * sigmoid_fast(l) : 0.f;
+    }
+    if (sig) d = live ? d * sigmoid_fast(-l) : 0.f;
+  }
+  float pa = 0.f;
+  if (f.cb != 0.f) {
+    for (int q = lane; q < N; q += 32) {
+      const float l = x.at(t, q);
+      if (masked_logit(l)) continue;
+      pa += (sig ? unit_sigmoid(l, low) : unit_softmax(l, r.m)) * inv_s * (f.cb * static_cast<float>(g.load[q]));
+    }
+    pa = warp_sum(pa);
+  }
+  const float lse = f.cz != 0.f ? f.cz * row_lse(r.m, r.z) : 0.f;
+  __syncwarp();
+  for (int q0 = 0; q0 < N; q0 += 32) {
+    const int q = q0 + lane;
+    float o = 0.f;
+    if (q < N) {
+      const float l = x.at(t, q);
+      if (!masked_logit(l)) {
+        const float p = dense || f.cb != 0.f || f.cz != 0.f ? unit_softmax(l, r.m) * inv_z : 0.f;
+        // (where p is 0 the row's sums take no part, finite or not)
+        if (dense && p != 0.f) o -= p * dot;
+        if (f.cb != 0.f) {
+          float ps = sig ? unit_sigmoid(l, low) * inv_s : p;
+          if (sig) ps *= sigmoid_fast(-l);
+          if (ps != 0.f) o += ps * (f.cb * static_cast<float>(g.load[q]) - pa);
+        }
+        if (p != 0.f) o += lse * p;
+      }
+    }
+    for (int j = 0; j < k; ++j) {
+      const int ej = __shfl_sync(FULL_MASK, e, j);
+      const float dj = __shfl_sync(FULL_MASK, d, j);
+      if (ej == q) o += dj;
+    }
+    if (q < N) {
+      const long long at = static_cast<long long>(t) * g.ld_out + q;
+      static_cast<Tl*>(g.out)[at] = from_f32<Tl>(o);
+    }
+  }
+  __syncwarp();
+}
 
 // A row in registers: the gradient of every logit is p_e (a_e + K) from the
 // losses and the plain softmax's gates (a_e = cb load_e, K the row's sums), and
@@ -552,9 +639,12 @@ __global__ __launch_bounds__(kGradWarps * 32, ROW ? kGradRowBlocks<S> : 4) void 
     }
     Tl* row_out = static_cast<Tl*>(g.out) + static_cast<long long>(t) * g.ld_out;
     const float K = lse - pa - dot;  // (softmax)
-    // Sums that are not finite (+inf logits under a z loss, such gradients from
-    // the caller) reach the experts that have a score, not 0 times them the rest.
-    const bool finite = fabsf(SIGMOID ? pa : K) < INFINITY;
+    // A row's sums that are not finite (+inf logits under a z loss, such
+    // gradients from the caller) are for route_backward_row, which keeps them
+    // from scores of 0.  The warp goes on there, since these rows are no common
+    // ones: a choice between the two for every logit took 1 us of 33.  (Sums of
+    // sigmoids are finite.)
+    if (ROW && !SIGMOID && __any_sync(FULL_MASK, has && !(fabsf(K) < INFINITY))) break;
 #pragma unroll
     for (int c = 0; c < S::C; ++c) {
       float o[S::CE];
@@ -570,8 +660,8 @@ __global__ __launch_bounds__(kGradWarps * 32, ROW ? kGradRowBlocks<S> : 4) void 
 #pragma unroll
         for (int i = 0; i < S::CE; ++i) {
           const int v = c * S::CE + i;
-          const float p = SIGMOID ? u[v] * inv * tt[v] : u[v] * inv;
-          if (finite || p != 0.f) o[i] = fmaf(p, SIGMOID ? a[i] - pa : a[i] + K, o[i]);
+          if constexpr (SIGMOID) o[i] = fmaf(u[v] * inv * tt[v], a[i] - pa, o[i]);
+          else o[i] = fmaf(u[v] * inv, a[i] + K, o[i]);
         }
         if constexpr (SIGMOID) {
           if (f.cz != 0.f) {
@@ -607,6 +697,12 @@ __global__ __launch_bounds__(kGradWarps * 32, ROW ? kGradRowBlocks<S> : 4) void 
       __syncwarp();
     }
   }
+  if constexpr (ROW && !SIGMOID) {
+    if (t0 >= T) return;
+    feed.drain(t0, step, T);
+    for (; t0 < T; t0 += step)
+      for (int t = t0; t < min(t0 + S::ROWS, T); ++t) route_backward_row(x, t, N, k, cfg, g, f, lane);
+  }
 }
 
 // Rows of more experts than registers hold: a warp a row, several passes.
@@ -616,84 +712,9 @@ __global__ __launch_bounds__(kGradWarps * 32) void route_backward_long_kernel(co
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   pdl_wait();
   pdl_trigger();
-  const bool sig = cfg.score == BFMOE_SCORE_SIGMOID;
-  const bool dense = g.dgates && !sig && !cfg.renorm;
   const LossFactors f(g, N, k);
-  for (int t = blockIdx.x * kGradWarps + w; t < T; t += gridDim.x * kGradWarps) {
-    RowSums r{-INFINITY, 0.f, 0.f};
-    if (g.load || dense) r = row_sums(x, t, N, lane, sig);
-    const float low = fminf(r.m, 0.f);
-    const float inv_z = r.z > 0.f ? 1.f / r.z : 0.f, inv_s = r.s > 0.f ? 1.f / r.s : 0.f;
-    int e = -1;
-    float d = 0.f, dot = 0.f;
-    if (g.dgates) {
-      float l = -INFINITY, dg = 0.f;
-      if (lane < k) {
-        e = g.idx[static_cast<long long>(t) * k + lane];
-        if (e < 0 || e >= N) {
-          report_error(BFMOE_EDEVICE_BOUNDS, static_cast<unsigned>(t));
-          e = -1;
-        } else {
-          l = x.at(t, e);
-          dg = g.dgates[static_cast<long long>(t) * k + lane] * cfg.scale;
-        }
-      }
-      const bool live = e >= 0 && !masked_logit(l) && !(g.bias && masked_logit(g.bias[e]));
-      if (!live) dg = 0.f;
-      if (dense) {
-        d = live ? unit_softmax(l, r.m) * inv_z * dg : 0.f;
-        dot = warp_sum(d);
-      } else if (cfg.renorm) {
-        const float m = warp_max(live ? l : -INFINITY);
-        const float u = !live ? 0.f : (sig ? unit_sigmoid(l, fminf(m, 0.f)) : unit_softmax(l, m));
-        const float s = warp_sum(u);
-        const float q = s > 0.f ? u / s : 0.f;
-        d = q * (dg - warp_sum(q * dg));
-      } else {
-        d = live ? dg * sigmoid_fast(l) : 0.f;
-      }
-      if (sig) d = live ? d * sigmoid_fast(-l) : 0.f;
-    }
-    float pa = 0.f;
-    if (f.cb != 0.f) {
-      for (int q = lane; q < N; q += 32) {
-        const float l = x.at(t, q);
-        if (masked_logit(l)) continue;
-        pa += (sig ? unit_sigmoid(l, low) : unit_softmax(l, r.m)) * inv_s * (f.cb * static_cast<float>(g.load[q]));
-      }
-      pa = warp_sum(pa);
-    }
-    const float lse = f.cz != 0.f ? f.cz * row_lse(r.m, r.z) : 0.f;
-    __syncwarp();
-    for (int q0 = 0; q0 < N; q0 += 32) {
-      const int q = q0 + lane;
-      float o = 0.f;
-      if (q < N) {
-        const float l = x.at(t, q);
-        if (!masked_logit(l)) {
-          const float p = dense || f.cb != 0.f || f.cz != 0.f ? unit_softmax(l, r.m) * inv_z : 0.f;
-          // (where p is 0 the row's sums take no part, finite or not)
-          if (dense && p != 0.f) o -= p * dot;
-          if (f.cb != 0.f) {
-            float ps = sig ? unit_sigmoid(l, low) * inv_s : p;
-            if (sig) ps *= sigmoid_fast(-l);
-            if (ps != 0.f) o += ps * (f.cb * static_cast<float>(g.load[q]) - pa);
-          }
-          if (p != 0.f) o += lse * p;
-        }
-      }
-      for (int j = 0; j < k; ++j) {
-        const int ej = __shfl_sync(FULL_MASK, e, j);
-        const float dj = __shfl_sync(FULL_MASK, d, j);
-        if (ej == q) o += dj;
-      }
-      if (q < N) {
-        const long long at = static_cast<long long>(t) * g.ld_out + q;
-        static_cast<Tl*>(g.out)[at] = from_f32<Tl>(o);
-      }
-    }
-    __syncwarp();
-  }
+  for (int t = blockIdx.x * kGradWarps + w; t < T; t += gridDim.x * kGradWarps)
+    route_backward_row(x, t, N, k, cfg, g, f, lane);
 }
 
 }  // namespace bfmoe

@@ -423,6 +423,14 @@ def test_backward_of_gate_gradients_that_are_not_finite(N):
                 assert (got[:, : N - 3] == 0).all(), (score, renorm, bad)
                 assert torch.isfinite(got[[0, 1, 3, 4]]).all()
                 assert not torch.isfinite(got[2]).all()
+            # the same of the losses: every expert that is left, in every row
+            load = torch.bincount(idx.flatten(), minlength=N + 1).int()
+            load[N] = T
+            for bad in ((float("nan"), 0.0), (0.0, float("nan")), (float("inf"), 0.1)):
+                got = B().bfmoe_route_backward(t.cuda(), idx, sc, dgates=torch.randn(T, k, device="cuda"), load=load,
+                                               dloss=torch.tensor(bad, device="cuda")).cpu()
+                assert (got[:, : N - 3] == 0).all(), (score, renorm, bad)
+                assert not torch.isfinite(got[:, N - 3:]).any()
 
 
 @pytest.mark.parametrize("N", [12, 250, 1024, 1300])
