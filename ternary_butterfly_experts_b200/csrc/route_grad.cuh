@@ -453,7 +453,8 @@ __device__ __noinline__ void route_backward_row(const Logits<Tl>& x, int t, int 
       const float u = !live ? 0.f : (sig ? unit_sigmoid(l, fminf(m, 0.f)) : unit_softmax(l, m));
       const float s = warp_sum(u);
       const float q = s > 0.f ? u / s : 0.f;
-      d = q * (dg - warp_sum(q * dg));
+      const float mean = warp_sum(q * dg);
+      d = q != 0.f ? q * (dg - mean) : 0.f;
     } else {
       d = live ? dg * sigmoid_fast(l) : 0.f;
     }
@@ -621,7 +622,8 @@ __global__ __launch_bounds__(kGradWarps * 32, ROW ? kGradRowBlocks<S> : 4) void 
         const float v = !live ? 0.f : (SIGMOID ? unit_sigmoid(le, fminf(top, 0.f)) : unit_softmax(le, top));
         const float s = seg_sum<LPR>(v);
         const float r = s > 0.f ? v * rcp_fast(s) : 0.f;
-        d = r * (dg - seg_sum<LPR>(r * dg));
+        const float mean = seg_sum<LPR>(r * dg);
+        d = r != 0.f ? r * (dg - mean) : 0.f;  // (a masked one has no part in a NaN either)
       } else {
         d = live ? dg * sigmoid_fast(le) : 0.f;
       }

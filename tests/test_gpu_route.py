@@ -413,7 +413,7 @@ def test_backward_of_gate_gradients_that_are_not_finite(N):
     t, _ = make_logits(T, N, "f32", N + 4)
     t[:, : N - 3] = float("-inf")
     for score in ("softmax", "sigmoid"):
-        for renorm in (False,):
+        for renorm in (True, False):
             sc = scoring(score, renorm=renorm)
             idx, gates = B().bfmoe_route(t.cuda(), k, sc, buckets=False)[:2]
             for bad in (float("nan"), float("inf")):
