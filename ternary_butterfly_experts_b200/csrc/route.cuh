@@ -113,6 +113,15 @@ __device__ __forceinline__ float value_eps(float eps_s, bool softmax, float scor
   return 0x1p-23f + eps_s * (softmax ? score : 1.f) + 0x1p-23f * fabsf(value);
 }
 
+// The bounds of a group's worth gv, the larger or the sum of the values a and b:
+// their errors go by their own sizes, which the sum of a positive and a negative
+// one does not show.
+__device__ __forceinline__ float group_eps(float eps_s, bool softmax, float a, float b) {
+  return 2.f * value_eps(eps_s, softmax, 1.f, fabsf(a) + (b > -INFINITY ? fabsf(b) : 0.f));
+}
+__device__ __forceinline__ float at_least(float gv, float eps) { return fabsf(gv) < INFINITY ? gv - eps : gv; }
+__device__ __forceinline__ float at_most(float gv, float eps) { return fabsf(gv) < INFINITY ? gv + eps : gv; }
+
 constexpr int kRouteWindow = 32;
 
 // Experts and gates of row t by one warp, decided in 64 bits: groups from
@@ -859,8 +868,10 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
       const bool real = gq < cfg.n_groups;
       bool in = real && rank < cfg.top_groups;
       if constexpr (SCORED) {
-        const float worst = -seg_max<LPR>(in ? -gv : -INFINITY), best = seg_max<LPR>(real && !in ? gv : -INFINITY);
-        clear = !(best > -INFINITY) || worst - best > 4.f * value_eps(eps_s, softmax, 1.f, worst);
+        const float eps = group_eps(eps_s, softmax, a, b);
+        const float worst = -seg_max<LPR>(in ? -at_least(gv, eps) : -INFINITY);
+        const float best = seg_max<LPR>(real && !in ? at_most(gv, eps) : -INFINITY);
+        clear = !(best > -INFINITY) || worst > best;
         if (!clear) in = (groups_64() >> gq) & 1ull;
         clear = true;
         if (!bias) {
@@ -895,7 +906,7 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
       __syncwarp();
       constexpr int GH = BFMOE_MAX_GROUPS / LPR;  // groups of a lane, at most
       const int hs = lsh == 0 ? (cfg.n_groups + LPR - 1) / LPR : 1;
-      float gv[GH];
+      float gv[GH], eps[GH];
       int rank[GH];
 #pragma unroll
       for (int h = 0; h < GH; ++h) {
@@ -919,6 +930,7 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
           a = fmaxf(a, oa);
         }
         gv[h] = top2 && b > -INFINITY ? a + b : a;
+        eps[h] = group_eps(eps_s, softmax, a, b);
       }
 #pragma unroll
       for (int h = 0; h < GH; ++h) {
@@ -941,15 +953,14 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
         if (h >= hs) continue;
         const bool real = gq + h * LPR < cfg.n_groups && (q & (lpg - 1)) == 0;
         const bool in = real && rank[h] < cfg.top_groups;
-        if (in) worst = fminf(worst, gv[h]);
-        else if (real) best = fmaxf(best, gv[h]);
+        if (in) worst = fminf(worst, at_least(gv[h], eps[h]));
+        else if (real) best = fmaxf(best, at_most(gv[h], eps[h]));
         kept |= static_cast<unsigned long long>(seg_bits<LPR>(in, lane)) << (h * LPR);
       }
       if constexpr (SCORED) {
         worst = -seg_max<LPR>(-worst);
         best = seg_max<LPR>(best);
-        // (a sum of two values; a score is at most 1)
-        clear = !(best > -INFINITY) || worst - best > 4.f * value_eps(eps_s, softmax, 1.f, worst);
+        clear = !(best > -INFINITY) || worst > best;
         if (!clear && fits_64) {
           const unsigned long long kept64 = groups_64();
           kept = 0ull;

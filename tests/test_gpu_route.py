@@ -192,6 +192,25 @@ def test_route_near_ties(N):
         check_route(torch.from_numpy(up), up.astype(np.float64), 8, **kw)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("N,G", [(64, 32), (64, 4), (120, 5), (256, 8), (256, 64), (1000, 10), (1024, 16), (2048, 16)])
+def test_route_near_groups_of_terms_that_cancel(N, G, score):
+    """Two experts a group, with biases of +1000 and -1000: float32 rounds each value by 3e-5, 64 bits rank sums that
+    are nearer than that."""
+    rng = np.random.default_rng(N + G)
+    T, per = 64, N // G
+    l = np.full((T, N), -np.inf, np.float32)
+    bias = np.zeros(N, np.float32)
+    spread = 3e-4 if score == "sigmoid" else 2e-4 * G   # of the logits: 7e-5 and more of the scores
+    for g in range(G):
+        a, b = g * per, g * per + per // 2 if per > 2 else g * per + 1
+        l[:, a] = rng.normal(size=T) * spread
+        l[:, b] = rng.normal(size=T) * spread
+        bias[a], bias[b] = 1000, -1000
+    check_route(torch.from_numpy(l), l.astype(np.float64), 2, score=score, bias=bias, groups=G, top_groups=G // 2,
+                group_score="top2")
+
+
 @pytest.mark.parametrize("shift", [-300.0, 25.0, 400.0, 5000.0])
 def test_route_shifted_logits(shift):
     """A shift of every logit changes no softmax; near values are ranked as in 64 bits all the same."""
