@@ -113,6 +113,11 @@ __device__ __forceinline__ float value_eps(float eps_s, bool softmax, float scor
   return 0x1p-23f + eps_s * (softmax ? score : 1.f) + 0x1p-23f * fabsf(value);
 }
 
+// A group's worth from its two best values.  A sum that leaves float32 at the
+// lower end (two biases of the lowest value) is not that of an empty group.
+__device__ __forceinline__ float group_worth(float a, float b, bool top2) {
+  return top2 && b > -INFINITY ? fmaxf(a + b, -0x1.fffffep127f) : a;
+}
 // The bounds of a group's worth gv, the larger or the sum of the values a and b:
 // their errors go by their own sizes, which the sum of a positive and a negative
 // one does not show.
@@ -855,7 +860,7 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
         b = fmaxf(fminf(a, oa), fmaxf(b, ob));
         a = fmaxf(a, oa);
       }
-      const float gv = top2 && b > -INFINITY ? a + b : a;
+      const float gv = group_worth(a, b, top2);
       int rank = 0;
 #pragma unroll 1
       for (int o0 = 0; o0 < cfg.n_groups; o0 += lpg) {  // the lanes of a group share the comparisons
@@ -929,7 +934,7 @@ __global__ __launch_bounds__(kRouteWarps * 32, kRouteBlocks<S>) void route_fast_
           b = fmaxf(fminf(a, oa), fmaxf(b, ob));
           a = fmaxf(a, oa);
         }
-        gv[h] = top2 && b > -INFINITY ? a + b : a;
+        gv[h] = group_worth(a, b, top2);
         eps[h] = group_eps(eps_s, softmax, a, b);
       }
 #pragma unroll

@@ -211,6 +211,22 @@ def test_route_near_groups_of_terms_that_cancel(N, G, score):
                 group_score="top2")
 
 
+@pytest.mark.parametrize("N", [16, 64, 100, 256, 1024, 2048])
+def test_route_groups_of_the_lowest_value(N):
+    """Two biases of the type's lowest value leave float32 when they are added up; such a group still comes before
+    one that has no expert left."""
+    per = N // 4
+    t, _ = make_logits(5, N, "f32", N)
+    t[:, : 2 * per] = float("-inf")
+    t[:, 3 * per + 3:] = float("-inf")
+    bias = np.zeros(N, np.float32)
+    bias[2 * per:3 * per] = np.finfo(np.float32).min
+    for score in ("softmax", "sigmoid"):
+        for renorm in (True, False):
+            check_route(t, t.double().numpy(), 4, score=score, renorm=renorm, bias=bias, groups=4, top_groups=2,
+                        group_score="top2")
+
+
 @pytest.mark.parametrize("shift", [-300.0, 25.0, 400.0, 5000.0])
 def test_route_shifted_logits(shift):
     """A shift of every logit changes no softmax; near values are ranked as in 64 bits all the same."""
