@@ -120,7 +120,9 @@ __global__ __launch_bounds__(kGradWarps * 32, kBalanceRowBlocks<S>) void balance
     if (!feed.take(x, t0, step, T, N, lane, l)) break;
     const int e_now = e;
     e = slot(t + step);
-    const float m = row_max<S>(l);
+    float m = row_max<S>(l);
+    // (a row past the end, anything, has no say in how the others are worked out)
+    if (SIGMOID && t >= T) m = 0.f;
     const bool some = t < T && m > -INFINITY;
     const float z = row_softmax<S>(l, m, u);
     float inv;
@@ -588,6 +590,7 @@ __global__ __launch_bounds__(kGradWarps * 32, ROW ? kGradRowBlocks<S> : 4) void 
       m = row_max<S>(l);
       float s = 0.f;
       if constexpr (SIGMOID) {
+        if (!has) m = 0.f;  // (past the end: no say in how the warp's other rows are worked out)
         if (f.cz != 0.f) {  // softmax_e lse cz is added at the end
           const float z = row_softmax<S>(l, m, u);
           lse = m > -INFINITY ? row_lse(m, z) * f.cz * rcp_fast(z) : 0.f;

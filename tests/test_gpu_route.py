@@ -562,6 +562,29 @@ def test_balance_loss(T, N, k, dtype):
     B().bfmoe_check_device_error()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,N", [(1, 200), (1, 104), (5, 128), (37, 256)])
+def test_results_do_not_depend_on_earlier_calls(T, N, dtype):
+    """Where a warp's rows reach behind the last one, what shared memory held before takes no part."""
+    t, _ = make_logits(T, N, dtype, T + N)
+    x = t.cuda()
+    idx = torch.topk(x.float(), 2)[1].int()
+    dg = torch.randn(T, 2, device="cuda")
+    dl = torch.tensor([0.3, 0.2], device="cuda")
+    sc = scoring("sigmoid")
+    first = None
+    for before in (0.0, 100.0, float("nan"), -60.0, 3.0):
+        big = torch.full((20000, N), before, dtype=x.dtype, device="cuda")
+        some = torch.zeros(20000, 2, dtype=torch.int32, device="cuda")
+        B().bfmoe_balance_loss(big, some, "sigmoid")
+        loss, load = B().bfmoe_balance_loss(x, idx, "sigmoid")
+        B().bfmoe_route_backward(big, some, sc, load=load, dloss=dl)
+        d = B().bfmoe_route_backward(x, idx, sc, dgates=dg, load=load, dloss=dl)
+        if first is None:
+            first = loss, d
+        assert torch.equal(loss, first[0]) and torch.equal(d, first[1]), before
+
+
 def test_load_of_two_halves_adds_up():
     """Two ranks' loads added up and a loss gradient each: the gradient of the whole batch."""
     T, N, k = 300, 64, 2
