@@ -449,15 +449,46 @@ class Scoring:
 
     def __init__(self, score: str = "softmax", n_groups: int = 1, top_groups: int = 1, group_score: str = "max",
                  renormalize: bool = True, scale: float = 1.0):
-        if score not in self.SCORES:
-            raise ValueError(f"score must be one of {sorted(self.SCORES)}, got {score!r}")
-        if group_score not in self.GROUP_SCORES:
-            raise ValueError(f"group_score must be one of {sorted(self.GROUP_SCORES)}, got {group_score!r}")
-        self.score, self.n_groups, self.top_groups, self.group_score = score, n_groups, top_groups, group_score
-        self.renormalize, self.scale = bool(renormalize), float(scale)
-        self.c = capi.BfmoeScoring(self.SCORES[score], n_groups, top_groups, self.GROUP_SCORES[group_score],
-                                   int(self.renormalize), self.scale)
+        self.c = capi.BfmoeScoring()   # holds every field, so that calls see a changed one
         self.ref = ctypes.byref(self.c)
+        self.score, self.n_groups, self.top_groups, self.group_score = score, n_groups, top_groups, group_score
+        self.renormalize, self.scale = renormalize, scale
+
+    @staticmethod
+    def _code(codes, name, value):
+        if value not in codes:
+            raise ValueError(f"{name} must be one of {sorted(codes)}, got {value!r}")
+        return codes[value]
+
+    @property
+    def score(self) -> str:
+        return next(s for s, code in self.SCORES.items() if code == self.c.score)
+
+    @score.setter
+    def score(self, value):
+        self.c.score = self._code(self.SCORES, "score", value)
+
+    @property
+    def group_score(self) -> str:
+        return next(s for s, code in self.GROUP_SCORES.items() if code == self.c.group_score)
+
+    @group_score.setter
+    def group_score(self, value):
+        self.c.group_score = self._code(self.GROUP_SCORES, "group_score", value)
+
+    n_groups = property(lambda self: self.c.n_groups, lambda self, value: setattr(self.c, "n_groups", value))
+    top_groups = property(lambda self: self.c.top_groups, lambda self, value: setattr(self.c, "top_groups", value))
+    renormalize = property(lambda self: bool(self.c.renormalize),
+                           lambda self, value: setattr(self.c, "renormalize", int(bool(value))))
+
+    @property
+    def scale(self) -> float:
+        return self._scale
+
+    @scale.setter
+    def scale(self, value):
+        self._scale = float(value)
+        self.c.scale = self._scale
 
     def __repr__(self):
         return (f"Scoring(score={self.score!r}, n_groups={self.n_groups}, top_groups={self.top_groups}, "

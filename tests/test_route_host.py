@@ -135,3 +135,25 @@ def test_grad_calls_refuse(L):
                 [(4096, 8191, 10, F32, F32)], [(4096, 8192, 10, F32, 3)]):
         assert c(*grads(*bad), 1.0, 64, *WS, None) == EINVAL, bad
     assert L.bfmoe_launch_count() == n0
+
+
+def test_a_changed_scoring_is_what_calls_see():
+    import ternary_butterfly_experts_b200 as B
+
+    sc = B.Scoring("sigmoid", n_groups=8, top_groups=4, group_score="top2", scale=2.5)
+    assert repr(sc) == ("Scoring(score='sigmoid', n_groups=8, top_groups=4, group_score='top2', renormalize=True, "
+                        "scale=2.5)")
+    new = dict(score="softmax", n_groups=4, top_groups=2, group_score="max", renormalize=False, scale=0.3)
+    for name, value in new.items():
+        setattr(sc, name, value)
+        assert getattr(sc, name) == value
+    c = ctypes.cast(sc.ref, ctypes.POINTER(capi.BfmoeScoring)).contents
+    assert (c.score, c.n_groups, c.top_groups, c.group_score, c.renormalize) == (0, 4, 2, 0, 0)
+    assert c.scale == ctypes.c_float(0.3).value
+    assert repr(sc) == repr(B.Scoring(**new))
+    for name, value in (("score", "tanh"), ("group_score", "sum")):
+        with pytest.raises(ValueError):
+            setattr(sc, name, value)
+        with pytest.raises(ValueError):
+            B.Scoring(**{name: value})
+    assert (sc.score, sc.group_score) == ("softmax", "max")
