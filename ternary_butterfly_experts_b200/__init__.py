@@ -705,7 +705,9 @@ def bfmoe_grad_workspace_size() -> int:
 class GradList:
     """A list of gradients (float32 or bfloat16, contiguous) for bfmoe_grad_norm
     and bfmoe_grad_clip, with its workspace: made once, used every step while
-    the tensors stay where they are.  ``out``: tensors of the same shapes that
+    the gradients are these very tensors.  (bfmoe_backward and
+    bfmoe_expert_backward return new ones each time: their list is made anew,
+    or the call is given the tensors themselves.)  ``out``: tensors of the same shapes that
     bfmoe_grad_clip writes instead of scaling in place (None entries: in place).
     Calls that overlap on the GPU need a list each (they share its workspace,
     which is made on the stream that is current here)."""

@@ -1,6 +1,8 @@
 """The operators together, as a training step and a serving step use them:
 logits, routing, experts, losses, gradients of experts, gates and logits, the
 clipped list; against the float64 oracles."""
+import os
+
 import numpy as np
 import pytest
 
@@ -131,6 +133,30 @@ def test_training_step(name, d, N, k, T, dtype, how):
     assert abs(float(norm) - ref) <= 1e-6 * ref
     after = S.grad_norm([t.double().cpu().numpy() for t in grads])
     assert abs(after - min(1.0, ref)) <= 1e-6
+
+
+def test_readme_example_clips_every_step():
+    """The README's Python example, its training part three times over (what is marked as made once: once)."""
+    m = B()
+    with open(os.path.join(os.path.dirname(__file__), "..", "README.md")) as f:
+        text = f.read()
+    code = text[text.index("```python") + len("```python"):]
+    first, step = code[:code.index("```")].split("# the same in a training step")
+    inp, _, x, wg, bias = setup(64, 16, 2, 40, "bf16", 5)
+    host = x.cpu().pin_memory()
+    env = dict(torch=torch, w_base_int8=inp.w_base, alpha=inp.alpha, theta=inp.theta, phi=inp.phi, w_gate=wg, bias=bias,
+               k=2, max_tokens=64, x=x, x_small=x[:3].contiguous(), x_pinned=host, y_pinned=torch.empty_like(host).pin_memory(),
+               bb=torch.randn(16, device="cuda") * 0.1, gy=torch.randn(40, 64, device="cuda"),
+               dloss=torch.tensor([0.01, 0.001], device="cuda"))
+    exec(first, env)
+    step = step[step.index("\n"):]
+    for i in range(3):
+        env["gy"] = torch.randn(40, 64, device="cuda") * (i + 1)
+        exec("\n".join(l for l in step.split("\n") if i == 0 or "made once" not in l), env)
+        g = env["grads"]
+        after = S.grad_norm([g[n].double().cpu().numpy() for n in ("dtheta", "dphi", "dw_base")])
+        assert float(env["norm"]) > 1 and abs(after - 1) <= 1e-6, (i, float(env["norm"]), after)
+    m.bfmoe_check_device_error()
 
 
 def test_expert_backward_is_backward_without_the_router():
