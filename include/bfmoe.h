@@ -489,7 +489,9 @@ int bfmoe_grad_norm(const bfmoe_grad* grads, int n, float* norm, void* ws, size_
 /*
  * The norm, and every gradient times min(1, max_norm / norm): in place, or
  * written to out (then out holds the gradients also where nothing is scaled).
- * A norm that is not finite scales nothing; it is there to be read in norm.
+ * Where an infinity or a NaN among the gradients leaves no norm, nothing is
+ * scaled, and norm says so.  A finite norm beyond float32 is written as +inf,
+ * too, but scales: the factor is that of the float64 norm.
  * Tensors that the call writes may overlap no other tensor of the list
  * (BFMOE_EINVAL).  max_norm >= 0.  Other arguments as for bfmoe_grad_norm.
  */

@@ -778,8 +778,9 @@ def bfmoe_grad_norm(grads, norm=None, stream=None):
 
 def bfmoe_grad_clip(grads, max_norm: float, norm=None, stream=None):
     """Scale a GradList (or a sequence of tensors, in place) by
-    min(1, max_norm / norm); returns the norm before it (float32 [1]).  A norm
-    that is not finite leaves the gradients as they are."""
+    min(1, max_norm / norm); returns the norm before it (float32 [1]).  An
+    infinity or a NaN among the gradients leaves them as they are; a norm beyond
+    float32 comes back as inf, too, but scales them."""
     g, norm, s = _grad_call(grads, norm, stream)
     capi.check(capi.lib().bfmoe_grad_clip(g.c, g.n, max_norm, norm.data_ptr(), g.ws.data_ptr(), g.ws.nbytes, s))
     return norm

@@ -2,7 +2,8 @@
 // norm: norm = sqrt(sum of the squares of every element of every tensor),
 // g' = g min(1, max_norm / norm).  Squares and their sum are float64, so that
 // neither large nor small gradients leave the range and long sums lose
-// nothing; the sums' order is fixed.  A norm that is not finite scales nothing.
+// nothing; the sums' order is fixed.  A norm that is not finite in float64
+// (infinities or NaN among the elements) scales nothing.
 //
 // The list travels in the kernel's parameters (no copy to the device, nothing
 // to keep alive for a captured graph): up to kGradsPerLaunch tensors a launch,

@@ -130,6 +130,19 @@ def test_norm_that_is_not_finite_scales_nothing(bad, dtype):
         assert torch.equal(torch.nan_to_num(g), torch.nan_to_num(o))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_norm_beyond_float32_is_inf_and_scales(dtype):
+    """The norm of finite gradients that float32 cannot hold: written as inf, the factor from float64."""
+    g = torch.tensor([3e38, -3e38, 1.5e38, 1e30], device="cuda").to(dtype)
+    want = g.double().cpu().numpy()
+    ref = S.grad_norm([want])
+    assert ref > 3.5e38
+    assert float(B().bfmoe_grad_clip([g], 2.0)) == float("inf")
+    want = want * (2.0 / ref)
+    tol = 2 * 2.0 ** -24 + HALF[dtype] + 1e-12
+    assert (np.abs(g.double().cpu().numpy() - want) <= tol * np.abs(want)).all()
+
+
 def test_zero_gradients_and_limits():
     g = torch.zeros(100, device="cuda")
     assert float(B().bfmoe_grad_clip([g], 0.0)) == 0.0 and (g == 0).all()
