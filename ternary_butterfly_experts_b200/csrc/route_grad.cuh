@@ -424,7 +424,7 @@ struct LossFactors {
 // The gradient of row t by one warp, in several passes over the row.
 template <typename Tl>
 __device__ __noinline__ void route_backward_row(const Logits<Tl>& x, int t, int N, int k, const RouteCfg& cfg,
-                                                const RouteGrad& g, const LossFactors& f, int lane) {
+                                                const RouteGrad& g, LossFactors f, int lane) {
   const bool sig = cfg.score == BFMOE_SCORE_SIGMOID;
   const bool dense = g.dgates && !sig && !cfg.renorm;
   RowSums r{-INFINITY, 0.f, 0.f};
@@ -511,9 +511,9 @@ __device__ __noinline__ void route_backward_row(const Logits<Tl>& x, int t, int 
 // bound by the latency of a row's sums and shared-memory passes (6 warps a
 // scheduler), not by memory.
 template <class S, typename Tl, bool SIGMOID, bool ROW>
-__global__ __launch_bounds__(kGradWarps * 32, ROW ? kGradRowBlocks<S> : 4) void route_backward_kernel(const Logits<Tl> x, int T, int N,
-                                                                                            int k, const RouteCfg cfg,
-                                                                                            const RouteGrad g) {
+__global__ __launch_bounds__(kGradWarps * 32, ROW ? kGradRowBlocks<S> : 4) void route_backward_kernel(
+    const __grid_constant__ Logits<Tl> x, int T, int N, int k, const __grid_constant__ RouteCfg cfg,
+    const __grid_constant__ RouteGrad g) {
   constexpr int LPR = S::LPR, V = S::V;
   extern __shared__ __align__(128) float grad_smem[];  // a [MAXN], the rows' chosen terms [warps * ROWS][MAXN], buffers
   __shared__ uint64_t full_s[kGradWarps * 2];
@@ -712,8 +712,10 @@ __global__ __launch_bounds__(kGradWarps * 32, ROW ? kGradRowBlocks<S> : 4) void 
 
 // Rows of more experts than registers hold: a warp a row, several passes.
 template <typename Tl>
-__global__ __launch_bounds__(kGradWarps * 32) void route_backward_long_kernel(const Logits<Tl> x, int T, int N, int k,
-                                                                              const RouteCfg cfg, const RouteGrad g) {
+__global__ __launch_bounds__(kGradWarps * 32) void route_backward_long_kernel(const __grid_constant__ Logits<Tl> x, int T,
+                                                                              int N, int k,
+                                                                              const __grid_constant__ RouteCfg cfg,
+                                                                              const __grid_constant__ RouteGrad g) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   pdl_wait();
   pdl_trigger();
