@@ -218,3 +218,38 @@ def test_losses(T, N, k, off, dtype):
         for _ in range(2):  # the same sums in the same order
             again = B().bfmoe_balance_loss(x, e.int(), score)
             assert torch.equal(again[0], loss) and torch.equal(again[1], load)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,N,k,off", [(40003, 64, 2, 0), (40003, 128, 4, 0), (40003, 256, 2, 0), (20011, 250, 4, 0),
+                                       (20011, 512, 4, 0), (20011, 1024, 4, 0), (20011, 1000, 3, 1)])
+def test_backward_goes_on_behind_rows_that_are_not_finite(T, N, k, off, dtype, in_place):
+    """Rows with a +inf logit under a z loss, and with a NaN gate gradient, here and there: every other row is as
+    ever, also those that their warp had on the way."""
+    x, l = make(T, N, dtype, T + N, off, special=False)
+    inf_rows = torch.arange(17, T, 1501, device="cuda")
+    nan_rows = torch.arange(801, T, 1501, device="cuda")
+    e, _ = plain_route(l, k, "softmax")
+    x[inf_rows, 5] = INF
+    dg = torch.randn(T, k, device="cuda")
+    dg[nan_rows, 0] = float("nan")
+    load, losses = torch.bincount(e.reshape(-1), minlength=N), (0.3, 0.7)
+    dl = torch.tensor(losses, dtype=torch.float32, device="cuda")
+    losses = [float(v) for v in dl]
+    got = B().bfmoe_route_backward(x, e.int(), B().Scoring("softmax", renormalize=False), dgates=dg, dloss=dl,
+                                   load=torch.cat([load, load.new_tensor([T])]).int(), dlogits=x if in_place else None)
+    B().bfmoe_check_device_error()
+    got = got.double()
+    assert torch.isinf(got[inf_rows, 5]).all() and torch.isnan(got[nan_rows]).all()
+    rest = torch.ones(N, dtype=torch.bool, device="cuda")
+    rest[5] = False
+    # nothing reaches the others of a +inf row but their own gate's term, which is 0 times it
+    assert (got[inf_rows][:, rest] == 0).all()
+    ok = torch.ones(T, dtype=torch.bool, device="cuda")
+    ok[inf_rows] = ok[nan_rows] = False
+    want, bound = plain_backward(l, e, "softmax", False, 1.0, dg.nan_to_num(), load, T, losses)
+    lim = steps(l) * bound + TINY
+    if dtype == "bf16":
+        lim = lim + 2.0 ** -8 * (want.abs() + lim)
+    assert ((got - want).abs() <= lim)[ok].all()
