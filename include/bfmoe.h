@@ -392,7 +392,10 @@ typedef struct {
  *   - gates: the scores of the chosen (no bias; 0 for a masked expert), over
  *     their sum when renormalize (all 0 where nothing is left), times scale.
  *     A score below the smallest normal float32 may come out as 0, here and in
- *     the losses and gradients below.
+ *     the losses and gradients below.  They are float32 arithmetic with the
+ *     hardware's approximate exponential and reciprocal: a gate is off by up to
+ *     (64 + 4 max|l|) 2^-24 of itself (softmax of 1024 logits: 2e-7, plain
+ *     float32 7e-8).
  *   logits    device [T] rows of N, ld elements apart (ld >= N), dtype
  *   balance_bias  device float [N] or NULL
  *   idx, gates, counts, offsets, rows: as bfmoe_router_topk writes them; the

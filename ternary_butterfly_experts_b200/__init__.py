@@ -3,7 +3,10 @@
 Functions carry the C ABI's names (include/bfmoe.h) and take torch tensors
 that live on the current CUDA device; torch only provides device memory and
 streams.  Every compute step runs in the library's CUDA kernels, and a missing
-library raises instead of falling back.
+library raises instead of falling back.  A call with ``stream`` runs on that
+stream and makes its outputs and scratch as under ``torch.cuda.stream(stream)``;
+ordering it with the streams that made its inputs and use its outputs is the
+caller's part.
 
 Each expert is W_i = B(phi_i) . W_base . B(theta_i)^T with one shared ternary
 base (ButterflyMoE technical summary, gist.science, section 2.1); inference
