@@ -394,8 +394,8 @@ typedef struct {
  *     A score below the smallest normal float32 may come out as 0, here and in
  *     the losses and gradients below.  They are float32 arithmetic with the
  *     hardware's approximate exponential and reciprocal: a gate is off by up to
- *     (64 + 4 max|l|) 2^-24 of itself (softmax of 1024 logits: 2e-7, plain
- *     float32 7e-8).
+ *     (64 + 4 max|l|) 2^-24 of itself (softmax of 1024 logits: 1.9e-7, plain
+ *     float32 5.6e-8).
  *   logits    device [T] rows of N, ld elements apart (ld >= N), dtype
  *   balance_bias  device float [N] or NULL
  *   idx, gates, counts, offsets, rows: as bfmoe_router_topk writes them; the
