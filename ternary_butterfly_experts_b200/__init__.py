@@ -15,7 +15,6 @@ applies B(theta)^T, the ternary product and B(phi) without forming W_i
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import struct
@@ -59,24 +58,22 @@ def _stream(stream=None):
     return torch.cuda.current_stream().cuda_stream
 
 
-_CURRENT = contextlib.nullcontext()
-
-
-def _on(stream):
-    """Where a call makes its outputs and scratch: in the memory pool of the
-    stream that it runs on.  A block of another stream's pool may still be in
-    use there, by work that this call is not ordered behind."""
-    return _CURRENT if stream is None else _torch().cuda.stream(stream)
-
-
-def _returned(stream, *tensors):
-    """Outputs made for a call on ``stream``: the caller, on the current
-    stream, uses them too, so they are not reused before that stream is done."""
-    if stream is not None:
-        here = _torch().cuda.current_stream()
-        for t in tensors:
-            if t is not None:
-                t.record_stream(here)
+def _made(stream, make, *args, **kw):
+    """make(*args): the tensors of a call on ``stream``, None for the current
+    one.  They come from the memory pool of the stream that the call runs on: a
+    block of another stream's pool may still be in use there, by work that this
+    call is not ordered behind.  The caller, on the current stream, uses them
+    too, so they are not reused before that stream is done."""
+    if stream is None:
+        return make(*args, **kw)
+    cuda = _torch().cuda
+    here = cuda.current_stream()
+    with cuda.stream(stream):
+        made = make(*args, **kw)
+    for t in made.values() if isinstance(made, dict) else made if isinstance(made, tuple) else (made,):
+        if t is not None:
+            t.record_stream(here)
+    return made
 
 
 def _ptr(t):
@@ -141,9 +138,7 @@ def bfmoe_pack_base(w, out=None, stream=None):
     if w.dim() != 2 or w.shape[0] != d:
         raise ValueError("w must be [d][d]")
     if out is None:
-        with _on(stream):
-            out = torch.empty((d, words_per_row(d)), dtype=torch.int32, device=w.device)
-        _returned(stream, out)
+        out = _made(stream, torch.empty, (d, words_per_row(d)), dtype=torch.int32, device=w.device)
     capi.check(capi.lib().bfmoe_pack_base(_ptr(w), d, _ptr(out), _stream(stream)))
     return out
 
@@ -153,32 +148,19 @@ def bfmoe_unpack_base(w_packed, d: int, out=None, stream=None):
     torch = _torch()
     _need(w_packed, "w_packed")
     if out is None:
-        with _on(stream):
-            out = torch.empty((d, d), dtype=torch.bfloat16, device=w_packed.device)
-        _returned(stream, out)
+        out = _made(stream, torch.empty, (d, d), dtype=torch.bfloat16, device=w_packed.device)
     capi.check(capi.lib().bfmoe_unpack_base(_ptr(w_packed), d, _ptr(out), _stream(stream)))
     return out
 
 
-def _routing_buffers(T, N, k, dev, stream, buckets=True):
-    """(idx, gates, counts, offsets, rows) for a call on ``stream``."""
+def _routing_buffers(T, N, k, dev, buckets=True):
+    """(idx, gates, counts, offsets, rows)."""
     torch = _torch()
-    with _on(stream):
-        out = (torch.empty((T, k), dtype=torch.int32, device=dev),
-               torch.empty((T, k), dtype=torch.float32, device=dev))
-        out += (torch.empty((N,), dtype=torch.int32, device=dev),
-                torch.empty((N + 1,), dtype=torch.int32, device=dev),
-                torch.empty((T * k,), dtype=torch.int32, device=dev)) if buckets else (None, None, None)
-    _returned(stream, *out)
-    return out
-
-
-def _like(x, stream):
-    """An output of x's shape and type for a call on ``stream``."""
-    with _on(stream):
-        y = _torch().empty_like(x)
-    _returned(stream, y)
-    return y
+    out = (torch.empty((T, k), dtype=torch.int32, device=dev),
+           torch.empty((T, k), dtype=torch.float32, device=dev))
+    return out + ((torch.empty((N,), dtype=torch.int32, device=dev),
+                   torch.empty((N + 1,), dtype=torch.int32, device=dev),
+                   torch.empty((T * k,), dtype=torch.int32, device=dev)) if buckets else (None, None, None))
 
 
 def bfmoe_router_topk(x, w_gate, bias, k: int, ws, out=None, stream=None, buckets: bool = True):
@@ -193,7 +175,7 @@ def bfmoe_router_topk(x, w_gate, bias, k: int, ws, out=None, stream=None, bucket
     N = w_gate.shape[0]
     dev = x.device
     if out is None:
-        out = _routing_buffers(T, N, k, dev, stream, buckets)
+        out = _made(stream, _routing_buffers, T, N, k, dev, buckets)
     idx, gates, counts, offsets, rows = out
     capi.check(capi.lib().bfmoe_router_topk(
         _ptr(x), _dtype_code(x), T, d, _ptr(w_gate), _ptr(bias), N, k, _ptr(idx), _ptr(gates),
@@ -217,7 +199,7 @@ def bfmoe_router_topk_noalloc(x, w_gate, bias, k: int, out=None, stream=None):
     N = w_gate.shape[0]
     dev = x.device
     if out is None:
-        out = _routing_buffers(T, N, k, dev, stream)
+        out = _made(stream, _routing_buffers, T, N, k, dev)
     idx, gates, counts, offsets, rows = out
     capi.check(capi.lib().bfmoe_router_topk_noalloc(
         _ptr(x), _dtype_code(x), T, d, _ptr(w_gate), _ptr(bias), N, k, _ptr(idx), _ptr(gates),
@@ -249,9 +231,7 @@ class Layer:
         this layer read them instead of rebuilding them per call."""
         torch = _torch()
         n = bfmoe_layer_tables_size(self.d, self.n_experts)
-        with _on(stream):
-            self.tables = torch.empty(max(n, 256), dtype=torch.uint8, device=self.theta.device)
-        _returned(stream, self.tables)
+        self.tables = _made(stream, torch.empty, max(n, 256), dtype=torch.uint8, device=self.theta.device)
         self.c.tables = None
         bfmoe_prepare_layer(self, self.tables, stream=stream)
         self.c.tables = self.tables.data_ptr()
@@ -270,9 +250,7 @@ class Layer:
         _need(w_gate, "w_gate", torch.float32)
         N, d = w_gate.shape
         n = int(capi.lib().bfmoe_gate_parts_size(N, d))
-        with _on(stream):
-            self.gate_parts = torch.empty(max(n, 256), dtype=torch.uint8, device=w_gate.device)
-        _returned(stream, self.gate_parts)
+        self.gate_parts = _made(stream, torch.empty, max(n, 256), dtype=torch.uint8, device=w_gate.device)
         capi.check(capi.lib().bfmoe_prepare_gate(_ptr(w_gate), N, d, _ptr(self.gate_parts), self.gate_parts.numel(),
                                                 _stream(stream)))
         self.c.gate_parts = self.gate_parts.data_ptr()
@@ -325,7 +303,7 @@ def bfmoe_forward(layer: Layer, x, k: int, idx, gates, offsets, rows, ws, y=None
     if d != layer.d:
         raise ValueError(f"x has width {d}, layer has d={layer.d}")
     if y is None:
-        y = _like(x, stream)
+        y = _made(stream, _torch().empty_like, x)
     capi.check(capi.lib().bfmoe_forward(
         ctypes.byref(layer.c), _ptr(x), _dtype_code(x), T, k, _ptr(idx), _ptr(gates), _ptr(offsets),
         _ptr(rows), _ptr(y), _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)))
@@ -343,7 +321,7 @@ def bfmoe_decode_forward(layer: Layer, x, k: int, idx, gates, y=None, stream=Non
     _need(idx, "idx", torch.int32)
     _need(gates, "gates", torch.float32)
     if y is None:
-        y = _like(x, stream)
+        y = _made(stream, _torch().empty_like, x)
     capi.check(capi.lib().bfmoe_decode_forward(
         ctypes.byref(layer.c), _ptr(x), _dtype_code(x), T, k, _ptr(idx), _ptr(gates), _ptr(y), _stream(stream)))
     return y
@@ -371,12 +349,11 @@ def bfmoe_backward(layer: Layer, x, k: int, w_gate, routing, gy, bias_grad: bool
     if ws is None:
         ws = _scratch(bfmoe_backward_workspace_size(d, N, T, k), dev, stream)
     f = dict(dtype=torch.float32, device=dev)
-    with _on(stream):
-        out = {"dx": torch.empty((T, d), **f), "dtheta": torch.empty_like(layer.theta),
-               "dphi": torch.empty_like(layer.phi), "dw_base": torch.empty((d, d), **f),
-               "dalpha": torch.empty((1,), **f), "dw_gate": torch.empty((N, d), **f),
-               "dbias": torch.empty((N,), **f) if bias_grad else None}
-    _returned(stream, *out.values())
+    out = _made(stream, lambda: {
+        "dx": torch.empty((T, d), **f), "dtheta": torch.empty_like(layer.theta),
+        "dphi": torch.empty_like(layer.phi), "dw_base": torch.empty((d, d), **f),
+        "dalpha": torch.empty((1,), **f), "dw_gate": torch.empty((N, d), **f),
+        "dbias": torch.empty((N,), **f) if bias_grad else None})
     capi.check(capi.lib().bfmoe_backward(
         ctypes.byref(layer.c), _ptr(x), _dtype_code(x), T, k, _ptr(w_gate), _ptr(idx), _ptr(gates), _ptr(offsets),
         _ptr(rows), _ptr(gy), _ptr(out["dx"]), _ptr(out["dtheta"]), _ptr(out["dphi"]), _ptr(out["dw_base"]),
@@ -402,9 +379,9 @@ def bfmoe_moe_forward(layer: Layer, x, w_gate, bias, k: int, ws, routing=None, y
     N = layer.n_experts
     dev = x.device
     if routing is None:
-        routing = _routing_buffers(T, N, k, dev, stream)
+        routing = _made(stream, _routing_buffers, T, N, k, dev)
     if y is None:
-        y = _like(x, stream)
+        y = _made(stream, _torch().empty_like, x)
     idx, gates, counts, offsets, rows = routing
     capi.check(capi.lib().bfmoe_moe_forward(
         ctypes.byref(layer.c), _ptr(x), _dtype_code(x), T, _ptr(w_gate), _ptr(bias), k, _ptr(idx), _ptr(gates),
@@ -543,9 +520,11 @@ def bfmoe_route_workspace_size(n_experts: int, T: int, k: int) -> int:
 
 
 def _scratch(n, dev, stream):
-    """A workspace of one call, freed when the call returns."""
+    """A workspace of one call, freed when the call returns (see _made)."""
     torch = _torch()
-    with _on(stream):
+    if stream is None:
+        return torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(stream):
         return torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
 
 
@@ -561,9 +540,7 @@ def bfmoe_router_logits(x, w_gate, bias=None, logits=None, ws=None, stream=None)
     _need_shape(bias, "bias", torch.float32, N)
     code = _dtype_code(x)
     if logits is None:
-        with _on(stream):
-            logits = torch.empty((T, N), dtype=torch.float32, device=x.device)
-        _returned(stream, logits)
+        logits = _made(stream, torch.empty, (T, N), dtype=torch.float32, device=x.device)
     _need_shape(logits, "logits", torch.float32, T, N)
     s = _here(stream, "x", x, "w_gate", w_gate, "bias", bias, "logits", logits, "ws", ws)
     if ws is None:
@@ -571,6 +548,12 @@ def bfmoe_router_logits(x, w_gate, bias=None, logits=None, ws=None, stream=None)
     capi.check(capi.lib().bfmoe_router_logits(_ptr(x), code, T, d, _ptr(w_gate), _ptr(bias), N, _ptr(logits),
                                               _ptr(ws), ws.numel(), s))
     return logits
+
+
+def _route_outputs(logits, T, N, k, buckets):
+    new, i32 = logits.new_empty, _torch().int32
+    out = (new((T, k), dtype=i32), new((T, k), dtype=_torch().float32))
+    return out + ((new(N, dtype=i32), new(N + 1, dtype=i32), new(T * k, dtype=i32)) if buckets else (None, None, None))
 
 
 def bfmoe_route(logits, k: int, scoring: Scoring, balance_bias=None, ws=None, out=None, buckets: bool = True,
@@ -583,11 +566,7 @@ def bfmoe_route(logits, k: int, scoring: Scoring, balance_bias=None, ws=None, ou
     code, T, N, ld = _logits(logits)
     _need_shape(balance_bias, "balance_bias", torch.float32, N)
     if out is None:
-        new, i32 = logits.new_empty, torch.int32
-        with _on(stream):
-            out = (new((T, k), dtype=i32), new((T, k), dtype=torch.float32))
-            out += (new(N, dtype=i32), new(N + 1, dtype=i32), new(T * k, dtype=i32)) if buckets else (None, None, None)
-        _returned(stream, *out)
+        out = _made(stream, _route_outputs, logits, T, N, k, buckets)
         idx, gates, counts, offsets, rows = out
         s = _here(stream, "logits", logits, "balance_bias", balance_bias, "ws", ws)
     else:
@@ -620,9 +599,8 @@ def bfmoe_balance_loss(logits, idx, score: str = "softmax", ws=None, out=None, s
     k = idx.shape[1]
     _need_shape(idx, "idx", torch.int32, T, k)
     if out is None:
-        with _on(stream):
-            out = (logits.new_empty(2, dtype=torch.float32), logits.new_empty(N + 1, dtype=torch.int32))
-        _returned(stream, *out)
+        out = (_made(stream, logits.new_empty, 2, dtype=torch.float32),
+               _made(stream, logits.new_empty, N + 1, dtype=torch.int32))
     loss, load = out
     _need_shape(loss, "loss", torch.float32, 2)
     _need_shape(load, "load", torch.int32, N + 1)
@@ -651,9 +629,7 @@ def bfmoe_route_backward(logits, idx, scoring: Scoring, dgates=None, load=None, 
     _need_shape(dloss, "dloss", torch.float32, 2)
     _need_shape(balance_bias, "balance_bias", torch.float32, N)
     if dlogits is None:
-        with _on(stream):
-            dlogits, ldd = logits.new_empty((T, N)), N
-        _returned(stream, dlogits)
+        dlogits, ldd = _made(stream, logits.new_empty, (T, N)), N
     else:
         if dlogits.dtype is not logits.dtype or dlogits.shape != logits.shape:
             raise ValueError("dlogits must match logits in shape and dtype")
@@ -689,11 +665,10 @@ def bfmoe_expert_backward(layer: "Layer", x, k: int, routing, gy, ws=None, strea
     if ws is None:
         ws = _scratch(bfmoe_backward_workspace_size(d, N, T, k), x.device, stream)
     f = dict(dtype=torch.float32, device=x.device)
-    with _on(stream):
-        out = {"dx": torch.empty((T, d), **f), "dtheta": torch.empty_like(layer.theta),
-               "dphi": torch.empty_like(layer.phi), "dw_base": torch.empty((d, d), **f),
-               "dalpha": torch.empty((1,), **f), "dgates": torch.empty((T, k), **f)}
-    _returned(stream, *out.values())
+    out = _made(stream, lambda: {
+        "dx": torch.empty((T, d), **f), "dtheta": torch.empty_like(layer.theta),
+        "dphi": torch.empty_like(layer.phi), "dw_base": torch.empty((d, d), **f),
+        "dalpha": torch.empty((1,), **f), "dgates": torch.empty((T, k), **f)})
     capi.check(capi.lib().bfmoe_expert_backward(
         ctypes.byref(layer.c), _ptr(x), _dtype_code(x), T, k, _ptr(idx), _ptr(gates), _ptr(offsets), _ptr(rows),
         _ptr(gy), _ptr(out["dx"]), _ptr(out["dtheta"]), _ptr(out["dphi"]), _ptr(out["dw_base"]), _ptr(out["dalpha"]),
@@ -758,15 +733,16 @@ def _grad_call(grads, norm, stream):
     """(GradList, norm, stream handle) of a call on the current device."""
     torch = _torch()
     g = grads
-    if not isinstance(g, GradList):
-        with _on(stream):  # the list's workspace goes when the call returns
-            g = GradList(grads)
-    elif stream is not None:
-        g.ws.record_stream(stream)
+    if stream is not None:
+        if not isinstance(g, GradList):
+            with torch.cuda.stream(stream):  # the list's workspace goes when the call returns
+                g = GradList(grads)
+        else:
+            g.ws.record_stream(stream)
+    elif not isinstance(g, GradList):
+        g = GradList(grads)
     if norm is None:
-        with _on(stream):
-            norm = g.ws.new_empty(1, dtype=torch.float32)
-        _returned(stream, norm)
+        norm = _made(stream, g.ws.new_empty, 1, dtype=torch.float32)
     else:
         _need_shape(norm, "norm", torch.float32, 1)
     return g, norm, _here(stream, "the gradients", g.ws, "norm", norm)
@@ -793,9 +769,7 @@ def bfmoe_materialize_expert(layer: Layer, e: int, out=None, stream=None):
     """alpha * B(phi_e) . W_base . B(theta_e)^T as float32 [d][d] (checking aid)."""
     torch = _torch()
     if out is None:
-        with _on(stream):
-            out = torch.empty((layer.d, layer.d), dtype=torch.float32, device=layer.theta.device)
-        _returned(stream, out)
+        out = _made(stream, torch.empty, (layer.d, layer.d), dtype=torch.float32, device=layer.theta.device)
     capi.check(capi.lib().bfmoe_materialize_expert(ctypes.byref(layer.c), e, _ptr(out), _stream(stream)))
     return out
 
@@ -915,8 +889,7 @@ class ButterflyMoE:
         if getattr(self, "_host_key", None) != key:
             code = BFMOE_BF16 if self.dtype == torch.bfloat16 else BFMOE_F32
             n = bfmoe_moe_host_workspace_size(self.layer.d, self.layer.n_experts, T, self.k, code, chunk)
-            self.ws_host = _scratch(n, self.layer.theta.device, stream)
-            _returned(stream, self.ws_host)
+            self.ws_host = _made(stream, torch.empty, max(n, 256), dtype=torch.uint8, device=self.layer.theta.device)
             self._host_key = key
         elif stream is not None:
             self.ws_host.record_stream(stream)
